@@ -5,12 +5,12 @@
 #include <stdio.h>
 #include <stdlib.h>
 
-#include "../../include/nvfp4.h"
+#include "api_util.h"
 #include "internal.h"
 
-namespace {
+namespace nvfp4 {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 nvfp4_status fail(nvfp4_status s, const char* fmt, ...) {
   va_list ap;
@@ -19,6 +19,8 @@ nvfp4_status fail(nvfp4_status s, const char* fmt, ...) {
   va_end(ap);
   return s;
 }
+
+const char* last_error() { return g_err; }
 
 nvfp4_status ok() {
   g_err[0] = '\0';
@@ -45,6 +47,16 @@ nvfp4_status check_k(int64_t K) {
     return fail(NVFP4_ERR_UNSUPPORTED, "K = %lld: the library needs K <= 4194304", (long long)K);
   return NVFP4_OK;
 }
+
+}  // namespace nvfp4
+
+namespace {
+
+using nvfp4::aligned;
+using nvfp4::check_k;
+using nvfp4::fail;
+using nvfp4::hip_status;
+using nvfp4::ok;
 
 // nvfp4_gemm and nvfp4_gemm_noalloc: the same checks, plans and kernels; the
 // second takes its split-K scratch from the library's fixed per-device array
@@ -118,7 +130,7 @@ nvfp4_status gemm_call(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, 
 
 extern "C" {
 
-const char* nvfp4_last_error(void) { return g_err; }
+const char* nvfp4_last_error(void) { return nvfp4::last_error(); }
 
 nvfp4_status nvfp4_force_plan(int32_t family, int32_t kind, int32_t splits) {
   if (family < 0 || family >= nvfp4::kForceFamilies)

@@ -34,7 +34,7 @@
 //    and stores bf16, then resets the counter.  Partials and counters are
 //    accessed only with agent-coherent operations, so no cache-wide fence
 //    is needed.  One launch, bitwise deterministic.
-//  * Register streaming: small-M tiles (k_gemm_kreg) and the grouped MoE
+//  * Register streaming: small-M tiles (k_gemm_kreg, main loop in kreg_tile.h) and the grouped MoE
 //    kernels (k_grouped_reg) load operands straight into VGPRs in whole
 //    128-byte lines per row, two or three 256-element K units ahead, and put
 //    them into MFMA layout with one DPP exchange; there the number of reads
@@ -48,7 +48,7 @@
 //    stages), so the stage loop issues no address arithmetic.
 //
 // Files: the LDS-staged tile kernel k_gemm and its helpers are in
-// gemm_tile.h; the two large-M 8-wave NVFP4 tiles are instantiated in
+// gemm_tile.h, the register-streamed main loop in kreg_tile.h; the two large-M 8-wave NVFP4 tiles are instantiated in
 // gemm_large.hip (built with another instruction schedule); this file holds
 // the other tiles, the register-streamed and grouped kernels, the plans and
 // the launchers.
@@ -62,8 +62,7 @@
 
 #include "device.h"
 #include "internal.h"
-
-#include "gemm_tile.h"
+#include "kreg_tile.h"
 
 namespace nvfp4 {
 
@@ -257,58 +256,6 @@ __global__ __launch_bounds__(C::kThreads, 1) void k_grouped_a16(GroupedLaunch p)
     store_bf16<C>(acc, tm_active, alpha, p.d + mc * p.N + n0, p.N, rows_c, B.rows);
   }
 }
-
-// Whole-line operand loads: two 16-byte loads per lane cover a 16-row block of
-// one 256-K unit (128 bytes per row) as 8 whole lines each, lane l reading row
-// l % 8 (words 0..3) and row 8 + l % 8 (words 4..7), chunk l / 8 of each.
-// Exchange with the lane 8 away in the same row of 16 so that lane 16 g + r
-// holds row r, chunk 2 g in words 0..3 and chunk 2 g + 1 in words 4..7: the
-// 16x16x32 MFMA operand layout, with K permuted the same way for A and B.
-__device__ __forceinline__ void kreg_exchange(uint32_t (&w)[8], bool lo8) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t p = w[j], q = w[4 + j];
-    const uint32_t give = lo8 ? q : p;
-    const uint32_t recv = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0x128, 0xF, 0xF, false);  // row_ror:8
-    w[j] = lo8 ? p : recv;
-    w[4 + j] = lo8 ? recv : q;
-  }
-}
-
-// Scale layouts the register-streamed kernels can read in place
-// (nvfp4_gemm_sf, nvfp4_grouped_gemm_sf): 0 linear [rows][K/16]; 1 the 128 x
-// 4 tiled layout (512-byte tiles of 128 rows x 4 scale columns, row-major
-// tile order; row r, column c at byte (r % 32) 16 + ((r % 128) / 32) 4 + c %
-// 4); 2 the 8 x 4 one (32-byte tiles of 8 rows x 4 columns; row r, column c
-// at byte (r % 8) 4 + c % 4).  In both tiled layouts the 4 scales of columns
-// 4 j .. 4 j + 3 of a row are one aligned word, the word a lane loads, so
-// only its address changes.
-template <int SFL>
-struct SfLayout {
-  static_assert(SFL >= 0 && SFL <= 2, "scale layout");
-  // bytes between consecutive 256-element units of one row (4 words)
-  static constexpr uint32_t kUnitStep = SFL == 0 ? 16 : (SFL == 1 ? 4 * 512 : 4 * 32);
-  // Rows [r0, r0 + rows_valid) of a scale matrix with lds = K/16 bytes per
-  // row (r0 counts rows from the matrix start, any alignment): a descriptor
-  // bounded by the bytes of the row groups those rows occupy, and the offset
-  // of word j of local row r in unit 0.
-  static __device__ __forceinline__ rsrc_t rsrc(const uint8_t* sf, int64_t r0, int rows_valid, int64_t lds) {
-    if constexpr (SFL == 0) return make_rsrc(sf + r0 * lds, (uint32_t)(rows_valid * lds));
-    else if constexpr (SFL == 1)
-      return make_rsrc(sf + (r0 >> 7) * 128 * lds, (uint32_t)(((r0 & 127) + rows_valid + 127) / 128 * 128 * lds));
-    else return make_rsrc(sf + (r0 >> 3) * 8 * lds, (uint32_t)(((r0 & 7) + rows_valid + 7) / 8 * 8 * lds));
-  }
-  static __device__ __forceinline__ uint32_t offset(int64_t r0, int r, int j, int64_t lds) {
-    if constexpr (SFL == 0) return (uint32_t)(r * lds + 4 * j);
-    else if constexpr (SFL == 1) {
-      const int q = (int)(r0 & 127) + r;
-      return (uint32_t)((q >> 7) * 128 * lds + 512 * j + (q & 31) * 16 + ((q >> 5) & 3) * 4);
-    } else {
-      const int q = (int)(r0 & 7) + r;
-      return (uint32_t)((q >> 3) * 8 * lds + 32 * j + (q & 7) * 4);
-    }
-  }
-};
 
 // ---------------------------------------------------------------------------
 // Grouped GEMM streaming B through registers.  Every B element is used by
@@ -798,89 +745,6 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
   }
 }
 
-// ---------------------------------------------------------------------------
-// Register-streamed K-group GEMM for small and mid M (no LDS staging).  A
-// work-group owns one BM x BN output tile and a K range (all of K, or split z
-// of S); its KS waves are K-groups: wave w takes the 256-element K units w,
-// w + KS, w + 2 KS, ... of the range.  Every lane loads its 16-byte code
-// chunks and scale words straight into registers, D units ahead, dequantises
-// them and issues 16x16x32 f16 MFMAs on its wave's full tile.  The KS partial
-// tiles are summed through LDS in wave order (deterministic); with S > 1 the
-// last split to finish sums the S partials in split order.
-//
-// A unit is 128 bytes of codes per row, one cache line.  Each 16-row block is
-// loaded with two instructions that each cover 8 whole lines: lane l reads
-// row l % 8 (then row 8 + l % 8), bytes 16 (l / 8) .. 16 (l / 8) + 15.  On a
-// cold call the number of outstanding requests per CU is what limits the
-// rate, and whole-line requests carry twice the bytes of the half lines a
-// 16-row instruction would fetch.  One DPP rotation by 8 lanes within each
-// row of 16 then gives lane l = 16 g + r row r with chunks 2 g (words 0..3)
-// and 2 g + 1 (words 4..7), K elements 64 g .. 64 g + 63 of the unit; its
-// scale word is bytes 4 g .. 4 g + 3 of the row's 16 unit scales.  MFMA t of
-// chunk c multiplies elements 8 t .. 8 t + 7 of that chunk, the same K set
-// for A and B.
-//
-// MX tiles (MXFP4: one E8M0 scale per 32 elements) use the same loads and
-// exchange and no dequantisation: chunk c of every lane (32 codes, one MX
-// block) is the lane's operand of one v_mfma_scale_f32_16x16x128_f8f6f4
-// (lane 16 g + r: row r, K block g of the MFMA; its scale operand's low byte
-// applies to that row and block; the output layout is that of the 16x16 f16
-// MFMA).  Lane 16 g + r loads scale word g / 2 of the row's 8 unit scales;
-// bytes 2 g and 2 g + 1 of the unit are those of its chunks.
-// ---------------------------------------------------------------------------
-template <int BM_, int BN_, int KS_, int D_, int OCC_, int MX_ = 0>
-struct KCfg {
-  static constexpr int BM = BM_, BN = BN_, KS = KS_, D = D_, OCC = OCC_;
-  static constexpr bool kMx = MX_ != 0;
-  static constexpr int SBLK = kMx ? 32 : 16;        // elements per scale
-  static constexpr int TM = BM / 16, TN = BN / 16;
-  static constexpr int kThreads = KS * 64;
-  static constexpr int kTileFloats = BM * BN;        // one wave's partial tile
-  static constexpr int kUnit = 256;                  // K elements per unit
-  static_assert(BM % 16 == 0 && BN % 16 == 0, "16-row MFMA blocks");
-  static_assert(KS >= 1 && KS <= 16, "waves per work-group");
-  static_assert(KS * kTileFloats * 4 <= 65536, "partial tiles fit in 64 KB of LDS");
-};
-
-template <class C>
-struct KRegs {
-  uint32_t aq[C::D][C::TM][8], bq[C::D][C::TN][8];  // two 16-byte code chunks as words
-  uint32_t as[C::D][C::TM], bs[C::D][C::TN];        // scale words (4 e4m3)
-};
-
-// Loads of unit `unit` into slot u; dead units (past the end of the range)
-// read out of range, which returns zero without a memory access, so every
-// iteration issues the same loads.
-template <class C, int SFL>
-__device__ __forceinline__ void kreg_load(KRegs<C>& R, int u, int unit, bool live, const rsrc_t& ra,
-                                          const rsrc_t& ras, const rsrc_t& rb, const rsrc_t& rbs,
-                                          const uint32_t (&va)[C::TM][2], const uint32_t (&vas)[C::TM],
-                                          const uint32_t (&vb)[C::TN][2], const uint32_t (&vbs)[C::TN]) {
-  constexpr uint32_t kOut = 0x80000000u;
-  const int so = unit * (C::kUnit / 2);
-  const int sso = unit * (SFL == 0 ? C::kUnit / C::SBLK : (int)SfLayout<SFL>::kUnitStep);
-#pragma unroll
-  for (int tm = 0; tm < C::TM; ++tm) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const u4_t v = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, live ? va[tm][h] : kOut, so, 0));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) R.aq[u][tm][4 * h + j] = v[j];
-    }
-    R.as[u][tm] = __builtin_amdgcn_raw_buffer_load_b32(ras, live ? vas[tm] : kOut, sso, 0);
-  }
-#pragma unroll
-  for (int tn = 0; tn < C::TN; ++tn) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const u4_t v = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, live ? vb[tn][h] : kOut, so, 0));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) R.bq[u][tn][4 * h + j] = v[j];
-    }
-    R.bs[u][tn] = __builtin_amdgcn_raw_buffer_load_b32(rbs, live ? vbs[tn] : kOut, sso, 0);
-  }
-}
-
 template <class C, int SFL = 0>
 __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::OCC))) void k_gemm_kreg(
     GemmLaunch p) {
@@ -891,121 +755,10 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
   const int L = xcd_remap(blockIdx.x, (int)(p.tiles_m * p.tiles_n) * S);
   const int tile = L / S, z = L % S;
   const int64_t m0 = (int64_t)(tile / tiles_n) * C::BM, n0 = (int64_t)(tile % tiles_n) * C::BN;
-  const int64_t ld = p.K / 2, lds = p.K / C::SBLK;
   const int rows_a = (int)min<int64_t>(C::BM, p.M - m0), rows_b = (int)min<int64_t>(C::BN, p.N - n0);
-  const rsrc_t ra = make_rsrc(p.a + m0 * ld, (uint32_t)(rows_a * ld));
-  const rsrc_t ras = SfLayout<SFL>::rsrc(p.a_sf, m0, rows_a, lds);
-  const rsrc_t rb = make_rsrc(p.b + n0 * ld, (uint32_t)(rows_b * ld));
-  const rsrc_t rbs = SfLayout<SFL>::rsrc(p.b_sf, n0, rows_b, lds);
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const int r_in = lane & 15, g = lane >> 4;
-  // code offsets: rows lane % 8 and 8 + lane % 8 of each 16-row block, bytes
-  // 16 (lane / 8) of the unit; scale word g (MX: g / 2) of row r_in
-  const int sw = C::kMx ? 4 * (g >> 1) : 4 * g;
-  uint32_t va[C::TM][2], vas[C::TM], vb[C::TN][2], vbs[C::TN];
-#pragma unroll
-  for (int tm = 0; tm < C::TM; ++tm) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = tm * 16 + 8 * h + (lane & 7);
-      va[tm][h] = r < rows_a ? (uint32_t)(r * ld + 16 * (lane >> 3)) : 0x80000000u;
-    }
-    const int r = tm * 16 + r_in;
-    if constexpr (SFL == 0) vas[tm] = r < rows_a ? (uint32_t)(r * lds + sw) : 0x80000000u;
-    else vas[tm] = r < rows_a ? SfLayout<SFL>::offset(m0, r, g, lds) : 0x80000000u;
-  }
-#pragma unroll
-  for (int tn = 0; tn < C::TN; ++tn) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = tn * 16 + 8 * h + (lane & 7);
-      vb[tn][h] = r < rows_b ? (uint32_t)(r * ld + 16 * (lane >> 3)) : 0x80000000u;
-    }
-    const int r = tn * 16 + r_in;
-    if constexpr (SFL == 0) vbs[tn] = r < rows_b ? (uint32_t)(r * lds + sw) : 0x80000000u;
-    else vbs[tn] = r < rows_b ? SfLayout<SFL>::offset(n0, r, g, lds) : 0x80000000u;
-  }
-  // this work-group's K units [u_lo, u_hi): all of K, or split z of S
-  const int nu_all = (int)(p.K / C::kUnit);
-  const int u_lo = (int)((int64_t)z * nu_all / S), u_hi = (int)((int64_t)(z + 1) * nu_all / S);
-  const int nu = u_hi - u_lo;
-  // every wave runs the same number of iterations (a multiple of D); units
-  // past the end are dead
-  const int per_wave = (nu + C::KS - 1) / C::KS;
-  const int iters = (per_wave + C::D - 1) / C::D * C::D;
   Mfma<16>::Acc acc[C::TM][C::TN];
-#pragma unroll
-  for (int tm = 0; tm < C::TM; ++tm)
-#pragma unroll
-    for (int tn = 0; tn < C::TN; ++tn) acc[tm][tn] = Mfma<16>::Acc{0.f, 0.f, 0.f, 0.f};
-  KRegs<C> R;
-#pragma unroll
-  for (int u = 0; u < C::D; ++u) {
-    const int unit = wave + u * C::KS;
-    kreg_load<C, SFL>(R, u, u_lo + unit, unit < nu, ra, ras, rb, rbs, va, vas, vb, vbs);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  const bool lo8 = (lane & 8) == 0;
-  for (int i0 = 0; i0 < iters; i0 += C::D) {
-#pragma unroll
-    for (int u = 0; u < C::D; ++u) {
-#pragma unroll
-      for (int tm = 0; tm < C::TM; ++tm) kreg_exchange(R.aq[u][tm], lo8);
-#pragma unroll
-      for (int tn = 0; tn < C::TN; ++tn) kreg_exchange(R.bq[u][tn], lo8);
-      if constexpr (C::kMx) {
-        typedef int v8i_t __attribute__((ext_vector_type(8)));
-        const int ssh = 16 * (g & 1);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          v8i_t bv[C::TN];
-          int sb[C::TN];
-#pragma unroll
-          for (int tn = 0; tn < C::TN; ++tn) {
-            const uint32_t* w = R.bq[u][tn] + 4 * c;
-            bv[tn] = v8i_t{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-            sb[tn] = (int)(R.bs[u][tn] >> (ssh + 8 * c));
-          }
-#pragma unroll
-          for (int tm = 0; tm < C::TM; ++tm) {
-            const uint32_t* w = R.aq[u][tm] + 4 * c;
-            const v8i_t av = v8i_t{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-            const int sa = (int)(R.as[u][tm] >> (ssh + 8 * c));
-#pragma unroll
-            for (int tn = 0; tn < C::TN; ++tn)
-              acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv[tn], acc[tm][tn], 4, 4, 0, sa, 0,
-                                                                             sb[tn]);
-          }
-        }
-      } else {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        h2_t asp[C::TM], bsp[C::TN];
-#pragma unroll
-        for (int tm = 0; tm < C::TM; ++tm) asp[tm] = e4m3x2_to_h2(R.as[u][tm] >> (16 * c));
-#pragma unroll
-        for (int tn = 0; tn < C::TN; ++tn) bsp[tn] = e4m3x2_to_h2(R.bs[u][tn] >> (16 * c));
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          h8_t bf[C::TN];
-#pragma unroll
-          for (int tn = 0; tn < C::TN; ++tn) bf[tn] = dequant8(R.bq[u][tn][4 * c + t], scale_pair(bsp[tn], t >> 1));
-#pragma unroll
-          for (int tm = 0; tm < C::TM; ++tm) {
-            const h8_t af = dequant8(R.aq[u][tm][4 * c + t], scale_pair(asp[tm], t >> 1));
-#pragma unroll
-            for (int tn = 0; tn < C::TN; ++tn) acc[tm][tn] = Mfma<16>::run(af, bf[tn], acc[tm][tn]);
-          }
-        }
-      }
-      }
-      // the slot's reload stays after its last reads (old and new contents
-      // share registers; no copies that would wait on the load)
-      __builtin_amdgcn_sched_barrier(0);
-      const int unit = wave + (i0 + u + C::D) * C::KS;
-      kreg_load<C, SFL>(R, u, u_lo + unit, unit < nu, ra, ras, rb, rbs, va, vas, vb, vbs);
-    }
-  }
+  kreg_accumulate<C, SFL>(p, m0, n0, rows_a, rows_b, z, S, acc);
   // K-group sum: wave w's partial tile at red[w][.], element (tm, tn, lane, j)
   // at ((tm * TN + tn) * 64 + lane) * 4 + j
   float* mine = red + wave * C::kTileFloats;
@@ -1095,15 +848,6 @@ typedef Cfg<32, 256, 1, 8, 16, 256, 2, 0, 1, 4> CfgGroupedReg;  // MoE experts, 
 typedef Cfg<64, 256, 1, 8, 16, 256, 2, 0, 1, 2> CfgGroupedReg64;  // the same with 64-row passes over each expert
 typedef Cfg<32, 256, 1, 8, 16, 256, 2, 0, 1, 4> CfgGroupedRegF;  // 32-row passes quantising A on load: 2 WGs per CU
 
-struct PlanKind {
-  const char* name;
-  int bm, bn, bk;
-  bool splitk;
-  bool kreg;  // register-streamed K-group kernel
-  bool mx;    // MXFP4 tile
-  int ks;     // K-groups (waves) of a register-streamed or K-group LDS tile
-  int d;      // register-streamed tiles: K units in flight per wave
-};
 static const PlanKind kKinds[] = {
     {"tile256x256_mfma32", 256, 256, 128, false},
     {"tile128x128_mfma32", 128, 128, 128, true},
@@ -1138,7 +882,6 @@ static const PlanKind kMxKinds[] = {
 static constexpr int kNumMxKinds = (int)(sizeof(kMxKinds) / sizeof(kMxKinds[0]));
 static constexpr int kNumKinds = (int)(sizeof(kKinds) / sizeof(kKinds[0]));
 
-static const int kCUs = 256;
 static_assert(kCounterBytes / 4 >= kCUs, "split-K runs only below kCUs tiles");
 static const int64_t kMaxPartialBytesPerTile = 256 * 1024;  // one CU reduces a tile
 
@@ -1156,7 +899,7 @@ void set_forced_plan(int family, int kind, int splits) {
   g_forced[family].store(kind < 0 ? 0 : (kind + 1) | ((splits < 0 ? 0 : splits) << 16));
 }
 
-static bool forced_plan(int family, int* kind, int* splits) {
+bool forced_plan(int family, int* kind, int* splits) {
   const int v = g_forced[family].load();
   if (v == 0) return false;
   *kind = (v & 0xFFFF) - 1;
@@ -1164,7 +907,7 @@ static bool forced_plan(int family, int* kind, int* splits) {
   return true;
 }
 
-static void plan_splits(GemmPlan& pl, const PlanKind& k, int64_t K, int forced) {
+void plan_splits(GemmPlan& pl, const PlanKind& k, int64_t K, int forced) {
   const int64_t tiles = pl.tiles_m * pl.tiles_n;
   const int64_t nk = K / k.bk;
   int64_t s = 1;
@@ -1231,7 +974,7 @@ static void plan_splits(GemmPlan& pl, const PlanKind& k, int64_t K, int forced) 
 // three times, then 128x128 tiles,
 // and tiles of 8 waves, 256x256 or 256x192, once either fills the CUs twice
 // (all staging 256 K per stage: whole 128-byte lines per row).
-GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
+GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, uint32_t kinds) {
   GemmPlan pl;
   int kind = -1;
   int forced_splits = 0;
@@ -1277,7 +1020,7 @@ GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
   }
   // a plan forced by nvfp4_force_plan (tuning sweeps and tests only)
   int fk = -1, fs = 0;
-  if (forced_plan(kForceGemm, &fk, &fs) && fk < kNumKinds) {
+  if (forced_plan(kForceGemm, &fk, &fs) && fk < kNumKinds && (kinds >> fk & 1)) {
     kind = fk;
     forced_splits = fs;
   }

@@ -56,8 +56,14 @@ struct Mfma<16> {
 };
 
 template <int BM_, int BN_, int WM_, int WN_, int MF_, int BK_, int STAGES_, int IL_ = 0, int KS_ = 1,
-          int OCC_ = 1, int SBLK_ = 16, int DW_ = 0, int SFL_ = 0>
+          int OCC_ = 1, int SBLK_ = 16, int DW_ = 0, int SFL_ = 0, int GATED_ = 0>
 struct Cfg {
+  // GATED: B holds two matrices one after the other (gate rows, then up
+  // rows).  The tile's LDS rows 0 .. BN / 2 - 1 are gate rows, the others the
+  // same up rows, and every wave takes the same columns of both: its column
+  // blocks 0 .. TN / 2 - 1 are gate, TN / 2 .. TN - 1 up, so a lane holds both
+  // factors of each of its products.
+  static constexpr bool kGated = GATED_ != 0;
   // SFL 2: the scales are in the 8 x 4 tiled layout (32-byte tiles of 8 rows
   // x 4 scale columns, row r and column c at byte (r % 8) 4 + c % 4, tiles
   // row-major).  One stage of 8 rows is then one run of 8 SB bytes, word-major
@@ -90,12 +96,18 @@ struct Cfg {
   static constexpr int kWN = BN / WN;        // cols per wave
   static constexpr int TM = kWM / MF;        // MFMA tiles per wave along M
   static constexpr int TN = kWN / MF;
+  static constexpr int kBRows = kGated ? BN / 2 : BN;  // tile rows of one B matrix
+  static constexpr int kBWave = kGated ? kWN / 2 : kWN;  // and of one wave in it
+  // LDS row of column block tn within the wave's rows
+  static constexpr int b_row(int tn) { return !kGated || tn < TN / 2 ? tn * MF : kBRows + (tn - TN / 2) * MF; }
   static constexpr int KG = 64 / MF;         // lane groups along K in one MFMA
   static constexpr int CH = BK / 32;         // 16-byte code chunks per row per stage
   static constexpr int RB = BK / 2;          // code bytes per row per stage
   static constexpr int SB = BK / SBLK;       // scale bytes per row per stage
   static constexpr int kSub = CH / KG;       // MFMA sub-steps per stage (4 K-steps each)
   static_assert(BM % (WM * MF) == 0 && BN % (WN * MF) == 0, "tile shape");
+  static_assert(!kGated || (TN % 2 == 0 && SBLK_ == 16 && SFL_ == 0 && STAGES_ == 2),
+                "gated tiles: NVFP4, linear scales, an even number of column blocks");
   static_assert(BK == 128 || BK == 256, "stage depth");
   static_assert(STAGES >= 2 && STAGES <= 8, "pipeline");
   static_assert(KS == 1 || KS == 2 || KS == 4, "K-groups");
@@ -222,6 +234,9 @@ struct Operand {
   int64_t ld;    // code bytes per row (K/2)
   int64_t lds;   // scale bytes per row (K/16)
   int rows;
+  // the second matrix of a gated tile's B (rows as for the first)
+  const uint8_t* data2 = nullptr;
+  const uint8_t* sf2 = nullptr;
 };
 
 template <class C>
@@ -248,6 +263,21 @@ __device__ __forceinline__ void issue_stage(Smem<C>& sm, int buf, const Operand&
   constexpr bool U = W < C::kWaves;
   if constexpr (U) wave = wave < W ? wave : -1;
   dma_tile<C::BM, C::RB, 16, C::MF, W, 0, U>(sm.a[buf], A.data, A.ld, A.rows, kt * C::RB, wave, lane, a_rows_dma);
+  if constexpr (C::kGated) {
+    // each matrix's half of the tile is a tile of its own; the waves' shares
+    // go on from one to the next
+    constexpr int R = C::kBRows;
+    typedef DmaShape<R, C::RB, 16> BH;
+    typedef DmaShape<R, C::SB, D::SV> BSH;
+    constexpr int B1 = D::A::kInst, B2 = B1 + BH::kInst, S0 = B2 + BH::kInst, S1 = S0 + D::AS::kInst,
+                  S2 = S1 + BSH::kInst;
+    dma_tile<R, C::RB, 16, C::MF, W, B1, U>(sm.b[buf], B.data, B.ld, B.rows, kt * C::RB, wave, lane);
+    dma_tile<R, C::RB, 16, C::MF, W, B2, U>(sm.b[buf] + R * C::RB, B.data2, B.ld, B.rows, kt * C::RB, wave, lane);
+    dma_tile<C::BM, C::SB, D::SV, 0, W, S0, U>(sm.asf[buf], A.sf, A.lds, A.rows, kt * C::SB, wave, lane);
+    dma_tile<R, C::SB, D::SV, 0, W, S1, U>(sm.bsf[buf], B.sf, B.lds, B.rows, kt * C::SB, wave, lane);
+    dma_tile<R, C::SB, D::SV, 0, W, S2, U>(sm.bsf[buf] + R * C::SB, B.sf2, B.lds, B.rows, kt * C::SB, wave, lane);
+    return;
+  }
   dma_tile<C::BN, C::RB, 16, C::MF, W, D::A::kInst, U>(sm.b[buf], B.data, B.ld, B.rows, kt * C::RB, wave, lane);
   if constexpr (C::SFL == 2) {
     // the operand's scale pointer is its first row's group (rows start on a
@@ -359,9 +389,9 @@ __device__ __forceinline__ ReadAddr<C> read_addr(const Smem<C>& sm) {
   const int gw = wave % C::kGroupWaves, kgrp = wave / C::kGroupWaves;
   const int wm = gw / C::WN, wn = gw % C::WN;
   const int r_in = lane % C::MF, g = lane / C::MF;
-  const int ra_row = wm * C::kWM + r_in, rb_row = wn * C::kWN + r_in;
+  const int ra_row = wm * C::kWM + r_in, rb_row = wn * C::kBWave + r_in;
   // the swizzle depends on the row's low bits only, which row blocks keep
-  static_assert(C::kWM % swz_period<C::CH, C::MF>() == 0 && C::kWN % swz_period<C::CH, C::MF>() == 0 &&
+  static_assert(C::kWM % swz_period<C::CH, C::MF>() == 0 && C::kBWave % swz_period<C::CH, C::MF>() == 0 &&
                     C::MF % swz_period<C::CH, C::MF>() == 0, "swizzle must not depend on the row block");
 #pragma unroll
   for (int ss = 0; ss < ReadAddr<C>::kS; ++ss) {
@@ -472,8 +502,8 @@ __device__ __forceinline__ void compute_stage(const Smem<C>& sm, const ReadAddr<
     });
     static_for<C::TN>([&](auto tnc) {
       constexpr int tn = decltype(tnc)::value;
-      ds_read128_at<BUF * C::BN * C::RB + tn * C::MF * C::RB>(bc[tn], ra.b[ss]);
-      ds_read_u16_at<BUF * C::BN * C::SB + tn * C::MF * C::SB>(bsw[tn], ra.bs + ss * kScaleStep);
+      ds_read128_at<BUF * C::BN * C::RB + C::b_row(tn) * C::RB>(bc[tn], ra.b[ss]);
+      ds_read_u16_at<BUF * C::BN * C::SB + C::b_row(tn) * C::SB>(bsw[tn], ra.bs + ss * kScaleStep);
     });
     lgkm_wait();
     h2_t asp[C::TM], bsp[C::TN];
@@ -801,11 +831,11 @@ __device__ __forceinline__ int xcd_remap(int b, int G) {
   return x * q + min(x, r) + i;
 }
 
-template <class C, bool SPLITK>
-__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::OCC))) void k_gemm(GemmLaunch p) {
-  __shared__ __attribute__((aligned(16))) SharedGemm<C> shm;
-  Smem<C>& sm = shm.pipe;
-  __shared__ int last_flag;
+// This work-group's output tile and K split.
+struct TileAt {
+  int tm, tn, tile, z;
+};
+__device__ __forceinline__ TileAt tile_at(const GemmLaunch& p) {
   const int S = p.splits;
   const int G = (int)(p.tiles_m * p.tiles_n) * S;
   const int L = xcd_remap(blockIdx.x, G);
@@ -816,7 +846,16 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
   const int first_m = (tile_l / band) * p.group_m;
   const int gm = min(p.group_m, tiles_m - first_m);
   const int tmi = first_m + (tile_l % band) % gm, tni = (tile_l % band) / gm;
-  const int tile = tmi * tiles_n + tni;
+  return TileAt{tmi, tni, tmi * tiles_n + tni, z};
+}
+
+template <class C, bool SPLITK>
+__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::OCC))) void k_gemm(GemmLaunch p) {
+  __shared__ __attribute__((aligned(16))) SharedGemm<C> shm;
+  Smem<C>& sm = shm.pipe;
+  __shared__ int last_flag;
+  const TileAt at = tile_at(p);
+  const int S = p.splits, z = at.z, tmi = at.tm, tni = at.tn, tile = at.tile;
 
   const int64_t m0 = (int64_t)tmi * C::BM, n0 = (int64_t)tni * C::BN;
   const int64_t ld = p.K / 2, lds = p.K / C::SBLK;

@@ -59,8 +59,29 @@ struct GemmPlan {
 // Plan families that nvfp4_force_plan can force (tuning sweeps and tests).
 constexpr int kForceGemm = 0, kForceMx = 1, kForceGrouped = 2, kForceFamilies = 3;
 void set_forced_plan(int family, int kind, int splits);
+// The plan forced for a family (false: none); splits 0 means the plan's own.
+bool forced_plan(int family, int* kind, int* splits);
 
-GemmPlan choose_plan(int64_t M, int64_t N, int64_t K);
+constexpr int kCUs = 256;
+
+// A kernel instantiation as the plans see it.
+struct PlanKind {
+  const char* name;
+  int bm, bn, bk;
+  bool splitk;
+  bool kreg;  // register-streamed K-group kernel
+  bool mx;    // MXFP4 tile
+  int ks;     // K-groups (waves) of a register-streamed or K-group LDS tile
+  int d;      // register-streamed tiles: K units in flight per wave
+};
+// Splits of K (forced when > 0) and the workspace they need, for a plan whose
+// tile counts are set.
+void plan_splits(GemmPlan& pl, const PlanKind& k, int64_t K, int forced);
+
+// kinds: bit k set if the caller has plan kind k (a forced plan outside the
+// set is ignored; the library's own choice is always one of kAutoKinds).
+constexpr uint32_t kAutoKinds = 1u << 9 | 1u << 10 | 1u << 11 | 1u << 12 | 1u << 14 | 1u << 15 | 1u << 16;
+GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, uint32_t kinds = ~0u);
 hipError_t launch_gemm(const GemmPlan& plan, GemmLaunch p, hipStream_t stream);
 // Whether an NVFP4 plan reads scales in tiled layout sf_layout in place: the
 // register tiles read both layouts, the automatic LDS tiles the 8 x 4 one;
