@@ -434,6 +434,131 @@ const char* nvfp4_mx_gemm_plan(int64_t M, int64_t N, int64_t K);
  */
 nvfp4_status nvfp4_force_plan(int32_t family, int32_t kind, int32_t splits);
 
+/*
+ * The dense transformer block around the GEMM: bias, activation and residual
+ * in the GEMM's epilogue, the two projections of a gated feed-forward in one
+ * kernel, and the norms before and after a block with its gate and residual.
+ * They are the dense counterparts of the MoE pieces above (the pages run the
+ * attention projections next to the experts, "When a Benchmark Crashes: The
+ * Elusive FP4 GEMM Comparison on Blackwell SM120", section "Assumptions
+ * Made"; they do not describe these steps).  Operands, alignment, K and
+ * workspaces are as for nvfp4_gemm; sums and every step of an epilogue are
+ * fp32 and the result is rounded once.
+ *
+ * Row strides (ld*) count elements; a stride of 0 means the row length.  Rows
+ * are accessed 16 bytes at a time when the bases are 16-byte aligned and the
+ * strides multiples of 8, else element by element (2-byte alignment is all
+ * that bf16 arguments need here).
+ */
+typedef enum {
+  NVFP4_ACT_NONE = 0,
+  NVFP4_ACT_RELU = 1,
+  NVFP4_ACT_GELU = 2,      /* x (1 + erf(x / sqrt 2)) / 2 */
+  NVFP4_ACT_GELU_TANH = 3, /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+  NVFP4_ACT_SILU = 4       /* x / (1 + exp(-x)) */
+} nvfp4_activation;
+
+/*
+ * nvfp4_gemm_epilogue:
+ *   D[m][n] = bf16_rne( act(alpha * sum_k xA[m][k] xB[n][k] + bias[n]) + beta * residual[m][n] )
+ * alpha: device fp32, NULL = 1; bias: bf16 [N] or NULL; act: nvfp4_activation;
+ * residual: bf16 [M][N] with row stride ldr, or NULL (beta, a host value, is
+ * then ignored); d: bf16 [M][N] with row stride ldd.  d may be residual (same
+ * pointer and stride), and must not otherwise overlap an input.  Columns N ..
+ * ldd - 1 of d are not written.  M == 0 or N == 0 is a successful no-op.
+ * workspace: nvfp4_gemm_epilogue_workspace_size(M, N, K) bytes, under the
+ * rules of nvfp4_gemm (zero-filled once, calls sharing it ordered on one
+ * stream: two captured graphs that share it must not run at the same time).
+ * ERR_SHAPE for an unknown act or a stride below N; ERR_UNSUPPORTED when the
+ * output has 2^31 tiles or more.
+ */
+nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
+                                 const float* alpha, const uint16_t* bias, int32_t act, const uint16_t* residual,
+                                 int64_t ldr, float beta, uint16_t* d, int64_t ldd, int64_t M, int64_t N, int64_t K,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+size_t nvfp4_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K);
+/* Name of the plan (static string): those of nvfp4_gemm. */
+const char* nvfp4_gemm_epilogue_plan(int64_t M, int64_t N, int64_t K);
+
+/*
+ * nvfp4_gemm_gated: both projections of a gated feed-forward, the activation
+ * and the product in one kernel:
+ *   g = alpha[0] * sum_k xA[m][k] xB[i][k]     + bias[i]
+ *   u = alpha[1] * sum_k xA[m][k] xB[I + i][k] + bias[I + i]
+ *   h[m][i] = bf16_rne( act(g) * u )
+ * b uint8 [2I][K/2] and b_sf [2I][K/16]: the I gate rows, then the I up rows
+ * (the order of nvfp4_moe_ffn); alpha: device fp32 [2] or NULL (both 1); bias:
+ * bf16 [2I] or NULL; act: NVFP4_ACT_SILU for SwiGLU; h: bf16 [M][I] with row
+ * stride ldh.  g and u are not rounded before the product.  Any I.
+ *
+ * nvfp4_gemm_gated_quantize: the same h, not rounded to bf16 but quantised to
+ * NVFP4 by the rules of nvfp4_quantize with the device encode scale *gs (NULL
+ * = 1): q uint8 [M][I/2] (8-byte aligned), sf uint8 [M][I/16].  I % 16 == 0.
+ *
+ * M == 0 or I == 0 is a successful no-op.  workspace:
+ * nvfp4_gemm_gated_workspace_size(M, I, K) bytes under the rules of
+ * nvfp4_gemm.  Errors as for nvfp4_gemm_epilogue.
+ */
+nvfp4_status nvfp4_gemm_gated(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
+                              const float* alpha, const uint16_t* bias, int32_t act, uint16_t* h, int64_t ldh,
+                              int64_t M, int64_t I, int64_t K, void* workspace, size_t workspace_bytes,
+                              void* stream);
+nvfp4_status nvfp4_gemm_gated_quantize(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
+                                       const float* alpha, const uint16_t* bias, int32_t act, const float* gs,
+                                       uint8_t* q, uint8_t* sf, int64_t M, int64_t I, int64_t K, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+size_t nvfp4_gemm_gated_workspace_size(int64_t M, int64_t I, int64_t K);
+const char* nvfp4_gemm_gated_plan(int64_t M, int64_t I, int64_t K);
+
+/*
+ * nvfp4_ffn: a dense gated feed-forward, the counterpart of nvfp4_moe_ffn:
+ *   h = NVFP4( act(g) * u, *gs_h )        (nvfp4_gemm_gated_quantize, K = H)
+ *   D = bf16_rne( alpha_d * h W_d^T + bias_d + beta * residual )   (nvfp4_gemm_epilogue, K = I)
+ * a, a_sf: the NVFP4 input [M][H]; w_gu, w_gu_sf: [2I][H/2] gate rows then up
+ * rows, alpha_gu fp32 [2], bias_gu bf16 [2I]; w_d, w_d_sf: [H][I/2], alpha_d
+ * fp32, bias_d bf16 [H]; residual, beta, d, ldr, ldd as in
+ * nvfp4_gemm_epilogue.  NULL is allowed for every alpha, bias, gs_h and the
+ * residual.  H % 256 == 0 and I % 256 == 0 (ERR_UNSUPPORTED otherwise).  The
+ * hidden layer lives in the workspace (nvfp4_ffn_workspace_size bytes,
+ * zero-filled once before its first use, then reusable for any sizes; not
+ * shared between calls that may overlap).  M == 0 is a successful no-op.
+ */
+nvfp4_status nvfp4_ffn(const uint8_t* a, const uint8_t* a_sf, const uint8_t* w_gu, const uint8_t* w_gu_sf,
+                       const float* alpha_gu, const uint16_t* bias_gu, int32_t act, const float* gs_h,
+                       const uint8_t* w_d, const uint8_t* w_d_sf, const float* alpha_d, const uint16_t* bias_d,
+                       const uint16_t* residual, int64_t ldr, float beta, uint16_t* d, int64_t ldd, int64_t M,
+                       int64_t H, int64_t I, void* workspace, size_t workspace_bytes, void* stream);
+size_t nvfp4_ffn_workspace_size(int64_t M, int64_t H, int64_t I);
+
+/*
+ * nvfp4_residual_norm: the norms after one block and before the next, with
+ * the block's gate and the residual, on bf16 [T][H] rows:
+ *   u = norm(x; post_weight, post_bias)  if post_weight, else x
+ *   r = beta * residual + gate * u       (gate: 1 if NULL; residual: 0 if NULL)
+ *   y = norm(r; weight, bias)
+ *   norm(v; w, b) = (v - m) * rstd * w + b,  rstd = 1 / sqrt(mean((v - m)^2) + eps)
+ * kind NVFP4_NORM_LAYER: m = mean(v); NVFP4_NORM_RMS: m = 0.  weight and bias
+ * may be NULL (1 and 0); post_bias needs post_weight.  gate: bf16, one row
+ * [H] for all rows when gate_group is 0, else [ceil(T / gate_group)][H], row
+ * t / gate_group for row t (a gate for each sequence or each token).
+ * Outputs, each NULL if not wanted (one at least is): r bf16 [T][H]; y bf16
+ * [T][H]; q uint8 [T][H/2] (8-byte aligned) with sf uint8 [T][H/16], the
+ * NVFP4 quantisation of y (not of its bf16 rounding) by the rules of
+ * nvfp4_quantize with the device encode scale *gs (NULL = 1), H % 16 == 0.  r
+ * may be x or residual (same pointer and stride); outputs must not otherwise
+ * overlap inputs or each other.  ldx, ldres, ldr, ldy: row strides of x,
+ * residual, r and y.  y is computed from the unrounded r.  Sums over a row and
+ * rstd are fp64, rounded once to fp32; the other steps fp32.  Any H >= 1; T ==
+ * 0 is a successful no-op.  No workspace.
+ */
+typedef enum { NVFP4_NORM_RMS = 0, NVFP4_NORM_LAYER = 1 } nvfp4_norm_kind;
+nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t* post_weight,
+                                 const uint16_t* post_bias, const uint16_t* gate, int64_t gate_group,
+                                 const uint16_t* residual, int64_t ldres, float beta, const uint16_t* weight,
+                                 const uint16_t* bias, float eps, int32_t kind, uint16_t* r, int64_t ldr,
+                                 uint16_t* y, int64_t ldy, const float* gs, uint8_t* q, uint8_t* sf, int64_t T,
+                                 int64_t H, void* stream);
+
 /* Message describing the calling thread's last error ("" if none). */
 const char* nvfp4_last_error(void);
 

@@ -23,7 +23,7 @@ STATUS = {0: "NVFP4_OK", 1: "NVFP4_ERR_NULL", 2: "NVFP4_ERR_SHAPE", 3: "NVFP4_ER
           4: "NVFP4_ERR_UNSUPPORTED", 5: "NVFP4_ERR_WORKSPACE", 6: "NVFP4_ERR_HIP"}
 
 # exported symbol -> (restype, argtypes)
-_vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_vp, _i64, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "nvfp4_gemm": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp]),
     "nvfp4_gemm_noalloc": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp]),
@@ -65,6 +65,21 @@ SIGNATURES = {
     "nvfp4_mx_gemm_plan": (ctypes.c_char_p, [_i64, _i64, _i64]),
     "nvfp4_force_plan": (ctypes.c_int, [_i32, _i32, _i32]),
     "nvfp4_last_error": (ctypes.c_char_p, []),
+    "nvfp4_gemm_epilogue": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _f32, _vp, _i64, _i64, _i64,
+                                           _i64, _vp, _sz, _vp]),
+    "nvfp4_gemm_epilogue_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "nvfp4_gemm_epilogue_plan": (ctypes.c_char_p, [_i64, _i64, _i64]),
+    "nvfp4_gemm_gated": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _i64, _i64, _i64, _vp, _sz,
+                                        _vp]),
+    "nvfp4_gemm_gated_quantize": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _i64, _i64,
+                                                 _vp, _sz, _vp]),
+    "nvfp4_gemm_gated_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "nvfp4_gemm_gated_plan": (ctypes.c_char_p, [_i64, _i64, _i64]),
+    "nvfp4_ffn": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _f32, _vp,
+                                 _i64, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "nvfp4_ffn_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "nvfp4_residual_norm": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _f32, _i32, _vp,
+                                           _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp]),
 }
 
 # nvfp4_force_plan families
@@ -501,3 +516,187 @@ def nvfp4_alpha_from_scales(gs_a, gs_b, alpha, count: int, stream=None):
                                        _ptr(alpha, 4 * _n(count), "alpha", f), count, _stream(stream))
     _check(st, "nvfp4_alpha_from_scales")
     return alpha
+
+
+# nvfp4_activation and nvfp4_norm_kind
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+NORM_RMS, NORM_LAYER = 0, 1
+
+
+class _Call:
+    """Marshalling of one block-operator call: every tensor is checked (on one
+    GPU, its type, its size, its strides) before its address is taken, and the
+    call is made on that GPU's stream."""
+    __slots__ = ("fn", "dev")
+
+    def __init__(self, fn: str):
+        self.fn, self.dev = fn, None
+
+    def _on(self, t, name):
+        if not getattr(t, "is_cuda", False):
+            raise Nvfp4Error(1, self.fn, f"{name} must be a GPU tensor")
+        dev = t.get_device()
+        if self.dev is None:
+            self.dev = dev
+        elif dev != self.dev:
+            raise Nvfp4Error(2, self.fn, f"{name} is on GPU {dev}, the call's other tensors on GPU {self.dev}")
+
+    def flat(self, t, nbytes: int, name: str, itemsize: int = 1):
+        """Address of a contiguous tensor of at least nbytes (None -> NULL)."""
+        if t is None:
+            return None
+        self._on(t, name)
+        if not t.is_contiguous():
+            raise Nvfp4Error(2, self.fn, f"{name} must be contiguous")
+        if itemsize > 1 and str(t.dtype) not in _TYPES[itemsize]:
+            raise Nvfp4Error(2, self.fn, f"{name} is {t.dtype}, not {_TYPES[itemsize][0]}")
+        if t.nbytes < nbytes:
+            raise Nvfp4Error(2, self.fn, f"{name} holds {t.nbytes} bytes, the call needs {nbytes}")
+        return t.data_ptr()
+
+    def rows(self, t, rows: int, cols: int, name: str):
+        """Address and row stride of a bf16 [rows][cols] tensor (None -> NULL):
+        2-D with unit column stride and any row stride, or contiguous."""
+        if t is None:
+            return None, 0
+        if t.dim() != 2 or t.shape[1] != cols:
+            return self.flat(t, 2 * _n(rows, cols), name, 2), 0
+        self._on(t, name)
+        if str(t.dtype) not in _TYPES[2]:
+            raise Nvfp4Error(2, self.fn, f"{name} is {t.dtype}, not {_TYPES[2][0]}")
+        if t.shape[0] < rows:
+            raise Nvfp4Error(2, self.fn, f"{name} holds {t.shape[0]} rows, the call needs {rows}")
+        ld, step = t.stride()
+        if t.shape[0] > 1 and ld < cols or cols > 1 and step != 1:
+            raise Nvfp4Error(2, self.fn, f"{name} needs unit column stride and a row stride of at least {cols}")
+        return t.data_ptr(), max(ld, cols)
+
+    def run(self, stream, *args):
+        import torch
+        dev = self.dev
+        if dev is None or dev == torch.cuda.current_device():
+            st = getattr(lib(), self.fn)(*args, _stream(stream))
+        else:
+            with torch.cuda.device(dev):
+                st = getattr(lib(), self.fn)(*args, _stream(stream))
+        _check(st, self.fn)
+
+
+_TYPES = {2: ("torch.bfloat16", "torch.int16", "torch.uint16"), 4: ("torch.float32",)}
+
+
+def nvfp4_gemm_epilogue_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().nvfp4_gemm_epilogue_workspace_size(M, N, K))
+
+
+def nvfp4_gemm_epilogue_plan(M: int, N: int, K: int) -> str:
+    return lib().nvfp4_gemm_epilogue_plan(M, N, K).decode()
+
+
+def nvfp4_gemm_gated_workspace_size(M: int, I: int, K: int) -> int:
+    return int(lib().nvfp4_gemm_gated_workspace_size(M, I, K))
+
+
+def nvfp4_gemm_gated_plan(M: int, I: int, K: int) -> str:
+    return lib().nvfp4_gemm_gated_plan(M, I, K).decode()
+
+
+def nvfp4_ffn_workspace_size(M: int, H: int, I: int) -> int:
+    return int(lib().nvfp4_ffn_workspace_size(M, H, I))
+
+
+def _workspace(need: int, device):
+    import torch
+    return nvfp4_workspace_init(torch.empty(need, dtype=torch.uint8, device=device)) if need else None
+
+
+def gemm_epilogue_workspace(M: int, N: int, K: int, device="cuda"):
+    """Allocate and zero-fill the workspace nvfp4_gemm_epilogue needs (None if none)."""
+    return _workspace(nvfp4_gemm_epilogue_workspace_size(M, N, K), device)
+
+
+def gemm_gated_workspace(M: int, I: int, K: int, device="cuda"):
+    """Allocate and zero-fill the workspace nvfp4_gemm_gated needs (None if none)."""
+    return _workspace(nvfp4_gemm_gated_workspace_size(M, I, K), device)
+
+
+def ffn_workspace(M: int, H: int, I: int, device="cuda"):
+    """Allocate and zero-fill the workspace nvfp4_ffn needs (None if none)."""
+    return _workspace(nvfp4_ffn_workspace_size(M, H, I), device)
+
+
+def nvfp4_gemm_epilogue(a, a_sf, b, b_sf, alpha, bias, act: int, residual, beta: float, d, M: int, N: int, K: int,
+                        workspace=None, stream=None):
+    """d = bf16(act(alpha * A B^T + bias) + beta * residual); see include/nvfp4.h.
+    bias: bf16 [N] or None; act: ACT_*; residual, d: bf16 [M][N], any row
+    stride (residual may be None, or d).  d is returned."""
+    c = _Call("nvfp4_gemm_epilogue")
+    pr, ldr = c.rows(residual, M, N, "residual")
+    pd, ldd = c.rows(d, M, N, "d")
+    c.run(stream, c.flat(a, _n(M, K) // 2, "a"), c.flat(a_sf, _n(M, K) // 16, "a_sf"), c.flat(b, _n(N, K) // 2, "b"),
+          c.flat(b_sf, _n(N, K) // 16, "b_sf"), c.flat(alpha, 4, "alpha", 4), c.flat(bias, 2 * _n(N), "bias", 2), act,
+          pr, ldr, beta, pd, ldd, M, N, K, c.flat(workspace, 0, "workspace"), _bytes(workspace))
+    return d
+
+
+def nvfp4_gemm_gated(a, a_sf, b, b_sf, alpha, bias, act: int, h, M: int, I: int, K: int, workspace=None,
+                     stream=None):
+    """h = bf16(act(g) * u), g and u the projections by the first and last I
+    rows of b [2I][K/2]; see include/nvfp4.h.  alpha: fp32 [2] or None; bias:
+    bf16 [2I] or None; h: bf16 [M][I], any row stride.  h is returned."""
+    c = _Call("nvfp4_gemm_gated")
+    ph, ldh = c.rows(h, M, I, "h")
+    c.run(stream, c.flat(a, _n(M, K) // 2, "a"), c.flat(a_sf, _n(M, K) // 16, "a_sf"), c.flat(b, _n(I, K), "b"),
+          c.flat(b_sf, _n(I, K) // 8, "b_sf"), c.flat(alpha, 8, "alpha", 4), c.flat(bias, 4 * _n(I), "bias", 2), act,
+          ph, ldh, M, I, K, c.flat(workspace, 0, "workspace"), _bytes(workspace))
+    return h
+
+
+def nvfp4_gemm_gated_quantize(a, a_sf, b, b_sf, alpha, bias, act: int, gs, q, sf, M: int, I: int, K: int,
+                              workspace=None, stream=None):
+    """nvfp4_gemm_gated with h quantised to NVFP4: q uint8 [M][I/2], sf uint8
+    [M][I/16], encode scale gs (fp32 [1] or None).  (q, sf) is returned."""
+    c = _Call("nvfp4_gemm_gated_quantize")
+    c.run(stream, c.flat(a, _n(M, K) // 2, "a"), c.flat(a_sf, _n(M, K) // 16, "a_sf"), c.flat(b, _n(I, K), "b"),
+          c.flat(b_sf, _n(I, K) // 8, "b_sf"), c.flat(alpha, 8, "alpha", 4), c.flat(bias, 4 * _n(I), "bias", 2), act,
+          c.flat(gs, 4, "gs", 4), c.flat(q, _n(M, I) // 2, "q"), c.flat(sf, _n(M, I) // 16, "sf"), M, I, K,
+          c.flat(workspace, 0, "workspace"), _bytes(workspace))
+    return q, sf
+
+
+def nvfp4_ffn(a, a_sf, w_gu, w_gu_sf, alpha_gu, bias_gu, act: int, gs_h, w_d, w_d_sf, alpha_d, bias_d, residual,
+              beta: float, d, M: int, H: int, I: int, workspace, stream=None):
+    """A dense gated feed-forward on an NVFP4 input [M][H] with an NVFP4 hidden
+    layer [M][I]: d = bf16(alpha_d * h W_d^T + bias_d + beta * residual); see
+    include/nvfp4.h.  d is returned."""
+    c = _Call("nvfp4_ffn")
+    pr, ldr = c.rows(residual, M, H, "residual")
+    pd, ldd = c.rows(d, M, H, "d")
+    hi = _n(H, I)
+    c.run(stream, c.flat(a, _n(M, H) // 2, "a"), c.flat(a_sf, _n(M, H) // 16, "a_sf"), c.flat(w_gu, hi, "w_gu"),
+          c.flat(w_gu_sf, hi // 8, "w_gu_sf"), c.flat(alpha_gu, 8, "alpha_gu", 4),
+          c.flat(bias_gu, 4 * _n(I), "bias_gu", 2), act, c.flat(gs_h, 4, "gs_h", 4), c.flat(w_d, hi // 2, "w_d"),
+          c.flat(w_d_sf, hi // 16, "w_d_sf"), c.flat(alpha_d, 4, "alpha_d", 4), c.flat(bias_d, 2 * _n(H), "bias_d", 2),
+          pr, ldr, beta, pd, ldd, M, H, I, c.flat(workspace, 0, "workspace"), _bytes(workspace))
+    return d
+
+
+def nvfp4_residual_norm(x, post_weight, post_bias, gate, gate_group: int, residual, beta: float, weight, bias,
+                        eps: float, kind: int, r, y, gs, q, sf, T: int, H: int, stream=None):
+    """r = beta * residual + gate * post_norm(x); y = norm(r), to bf16 (r, y)
+    and NVFP4 (q, sf with encode scale gs); see include/nvfp4.h.  x, residual,
+    r, y: bf16 [T][H], any row stride; post_weight, post_bias, weight, bias:
+    bf16 [H]; gate: bf16 [H] (gate_group 0) or [ceil(T / gate_group)][H]; every
+    tensor but x may be None, one output at least is given.  (r, y, q, sf) is
+    returned."""
+    c = _Call("nvfp4_residual_norm")
+    gates = 0 if gate_group < 0 else 1 if gate_group == 0 else -(-T // gate_group)
+    px, ldx = c.rows(x, T, H, "x")
+    ps, lds = c.rows(residual, T, H, "residual")
+    pr, ldr = c.rows(r, T, H, "r")
+    py, ldy = c.rows(y, T, H, "y")
+    c.run(stream, px, ldx, c.flat(post_weight, 2 * _n(H), "post_weight", 2), c.flat(post_bias, 2 * _n(H), "post_bias", 2),
+          c.flat(gate, 2 * _n(gates, H), "gate", 2), gate_group, ps, lds, beta, c.flat(weight, 2 * _n(H), "weight", 2),
+          c.flat(bias, 2 * _n(H), "bias", 2), eps, kind, pr, ldr, py, ldy, c.flat(gs, 4, "gs", 4),
+          c.flat(q, _n(T, H) // 2, "q"), c.flat(sf, _n(T, H) // 16, "sf"), T, H)
+    return r, y, q, sf

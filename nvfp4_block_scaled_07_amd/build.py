@@ -4,9 +4,10 @@ Run ``python -m nvfp4_block_scaled_07_amd.build`` (or call :func:`build`).
 The quantiser needs IEEE fp32 semantics, so there is no fast-math, fp
 contraction is off and fp32 division stays correctly rounded.  Packed fp32
 instructions are disabled for all device code.  ``gemm_large.hip`` (the two
-large-M NVFP4 tiles) is compiled first, to an object of its own, with the
-iterative ILP instruction scheduler; the rest is compiled and linked with it
-in one hipcc call.
+large-M NVFP4 tiles) is compiled to an object of its own, with the iterative
+ILP instruction scheduler, and so is each source of the block operators
+(``csrc/block``), all at the same time as the rest; one last hipcc call links
+them.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import os
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +24,13 @@ LIB = os.path.join(PKG, "libnvfp4_gfx950.so")
 SOURCES = ["api.hip", "gemm.hip", "layout.hip", "moe.hip", "quantize.hip"]
 # sources compiled separately, with extra flags
 SCHED_SOURCES = {"gemm_large.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]}
+# the block operators, each source an object of its own, with its extra flags
+BLOCK_SOURCES = {
+    "block/block_api.hip": [],
+    "block/norm.hip": [],
+    "block/gemm_epilogue.hip": [],
+    "block/gemm_epilogue_large.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
+}
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -33,18 +42,22 @@ FLAGS = [
 ]
 
 
+def _object(objdir: str, src: str) -> str:
+    return os.path.join(objdir, os.path.splitext(os.path.basename(src))[0] + ".o")
+
+
 def object_commands(objdir: str) -> list:
-    """hipcc calls that compile each of SCHED_SOURCES to an object in objdir."""
+    """hipcc calls that compile every source to an object in objdir."""
     flags = [f for f in FLAGS if f != "-shared"]
-    return [[HIPCC, *flags, *extra, "-c", os.path.join(CSRC, src),
-             "-o", os.path.join(objdir, os.path.splitext(src)[0] + ".o")]
-            for src, extra in SCHED_SOURCES.items()]
+    sources = {**{s: [] for s in SOURCES}, **SCHED_SOURCES, **BLOCK_SOURCES}
+    return [[HIPCC, *flags, *extra, "-c", os.path.join(CSRC, src), "-o", _object(objdir, src)]
+            for src, extra in sources.items()]
 
 
 def command(out: str = LIB, objdir: str = "") -> list:
-    objs = [os.path.join(objdir, os.path.splitext(s)[0] + ".o") for s in SCHED_SOURCES]
-    # "-x none": the objects are linked, not compiled as HIP
-    return [HIPCC, *FLAGS, *[os.path.join(CSRC, s) for s in SOURCES], "-x", "none", *objs, "-o", out]
+    """The hipcc call that links the objects in objdir."""
+    objs = [_object(objdir, s) for s in [*SOURCES, *SCHED_SOURCES, *BLOCK_SOURCES]]
+    return [HIPCC, *FLAGS, *objs, "-o", out]
 
 
 def _run(cmd: list, verbose: bool) -> None:
@@ -64,8 +77,9 @@ def build(verbose: bool = False) -> str:
     """Compile every HIP source into the in-tree library; returns its path."""
     tmp = LIB + ".tmp"
     with tempfile.TemporaryDirectory(prefix="nvfp4_build_") as objdir:
-        for cmd in object_commands(objdir):
-            _run(cmd, verbose)
+        with ThreadPoolExecutor(len(os.sched_getaffinity(0))) as pool:
+            for done in [pool.submit(_run, cmd, verbose) for cmd in object_commands(objdir)]:
+                done.result()
         _run(command(tmp, objdir), verbose)
     os.replace(tmp, LIB)
     return LIB
