@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function passes device pointers, sizes and
 the current HIP stream to the C ABI of ``libnvfp4_gfx950.so`` (built in-tree by
-``nvfp4_block_scaled_07_amd.build``).  All arithmetic runs in the library's
+``nvfp4_block_scaled_07_amd.build``); the block operators' calls are marshalled
+by a native module (``_binding.so``, built with it), the others by ctypes.  All arithmetic runs in the library's
 HIP kernels; there is no CPU or PyTorch fallback, and a missing library is an
 error.
 
@@ -523,66 +524,24 @@ ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 NORM_RMS, NORM_LAYER = 0, 1
 
 
-class _Call:
-    """Marshalling of one block-operator call: every tensor is checked (on one
-    GPU, its type, its size, its strides) before its address is taken, and the
-    call is made on that GPU's stream."""
-    __slots__ = ("fn", "dev")
-
-    def __init__(self, fn: str):
-        self.fn, self.dev = fn, None
-
-    def _on(self, t, name):
-        if not getattr(t, "is_cuda", False):
-            raise Nvfp4Error(1, self.fn, f"{name} must be a GPU tensor")
-        dev = t.get_device()
-        if self.dev is None:
-            self.dev = dev
-        elif dev != self.dev:
-            raise Nvfp4Error(2, self.fn, f"{name} is on GPU {dev}, the call's other tensors on GPU {self.dev}")
-
-    def flat(self, t, nbytes: int, name: str, itemsize: int = 1):
-        """Address of a contiguous tensor of at least nbytes (None -> NULL)."""
-        if t is None:
-            return None
-        self._on(t, name)
-        if not t.is_contiguous():
-            raise Nvfp4Error(2, self.fn, f"{name} must be contiguous")
-        if itemsize > 1 and str(t.dtype) not in _TYPES[itemsize]:
-            raise Nvfp4Error(2, self.fn, f"{name} is {t.dtype}, not {_TYPES[itemsize][0]}")
-        if t.nbytes < nbytes:
-            raise Nvfp4Error(2, self.fn, f"{name} holds {t.nbytes} bytes, the call needs {nbytes}")
-        return t.data_ptr()
-
-    def rows(self, t, rows: int, cols: int, name: str):
-        """Address and row stride of a bf16 [rows][cols] tensor (None -> NULL):
-        2-D with unit column stride and any row stride, or contiguous."""
-        if t is None:
-            return None, 0
-        if t.dim() != 2 or t.shape[1] != cols:
-            return self.flat(t, 2 * _n(rows, cols), name, 2), 0
-        self._on(t, name)
-        if str(t.dtype) not in _TYPES[2]:
-            raise Nvfp4Error(2, self.fn, f"{name} is {t.dtype}, not {_TYPES[2][0]}")
-        if t.shape[0] < rows:
-            raise Nvfp4Error(2, self.fn, f"{name} holds {t.shape[0]} rows, the call needs {rows}")
-        ld, step = t.stride()
-        if t.shape[0] > 1 and ld < cols or cols > 1 and step != 1:
-            raise Nvfp4Error(2, self.fn, f"{name} needs unit column stride and a row stride of at least {cols}")
-        return t.data_ptr(), max(ld, cols)
-
-    def run(self, stream, *args):
-        import torch
-        dev = self.dev
-        if dev is None or dev == torch.cuda.current_device():
-            st = getattr(lib(), self.fn)(*args, _stream(stream))
-        else:
-            with torch.cuda.device(dev):
-                st = getattr(lib(), self.fn)(*args, _stream(stream))
-        _check(st, self.fn)
+_bind = None
 
 
-_TYPES = {2: ("torch.bfloat16", "torch.int16", "torch.uint16"), 4: ("torch.float32",)}
+def _native():
+    """The native marshalling module of the block operators (csrc/binding.cpp),
+    bound to the loaded library; raises if it has not been built."""
+    global _bind
+    if _bind is None:
+        import torch  # noqa: F401  (the module's tensor types)
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError(f"{PKG}/_binding.so is missing: run `python -m nvfp4_block_scaled_07_amd.build`") from e
+        names = ("nvfp4_last_error", "nvfp4_gemm_epilogue", "nvfp4_gemm_gated", "nvfp4_gemm_gated_quantize", "nvfp4_ffn",
+                 "nvfp4_residual_norm")
+        _binding.setup(Nvfp4Error, *[ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names])
+        _bind = _binding
+    return _bind
 
 
 def nvfp4_gemm_epilogue_workspace_size(M: int, N: int, K: int) -> int:
@@ -630,12 +589,7 @@ def nvfp4_gemm_epilogue(a, a_sf, b, b_sf, alpha, bias, act: int, residual, beta:
     """d = bf16(act(alpha * A B^T + bias) + beta * residual); see include/nvfp4.h.
     bias: bf16 [N] or None; act: ACT_*; residual, d: bf16 [M][N], any row
     stride (residual may be None, or d).  d is returned."""
-    c = _Call("nvfp4_gemm_epilogue")
-    pr, ldr = c.rows(residual, M, N, "residual")
-    pd, ldd = c.rows(d, M, N, "d")
-    c.run(stream, c.flat(a, _n(M, K) // 2, "a"), c.flat(a_sf, _n(M, K) // 16, "a_sf"), c.flat(b, _n(N, K) // 2, "b"),
-          c.flat(b_sf, _n(N, K) // 16, "b_sf"), c.flat(alpha, 4, "alpha", 4), c.flat(bias, 2 * _n(N), "bias", 2), act,
-          pr, ldr, beta, pd, ldd, M, N, K, c.flat(workspace, 0, "workspace"), _bytes(workspace))
+    (_bind or _native()).gemm_epilogue(a, a_sf, b, b_sf, alpha, bias, act, residual, beta, d, M, N, K, workspace, stream)
     return d
 
 
@@ -644,11 +598,7 @@ def nvfp4_gemm_gated(a, a_sf, b, b_sf, alpha, bias, act: int, h, M: int, I: int,
     """h = bf16(act(g) * u), g and u the projections by the first and last I
     rows of b [2I][K/2]; see include/nvfp4.h.  alpha: fp32 [2] or None; bias:
     bf16 [2I] or None; h: bf16 [M][I], any row stride.  h is returned."""
-    c = _Call("nvfp4_gemm_gated")
-    ph, ldh = c.rows(h, M, I, "h")
-    c.run(stream, c.flat(a, _n(M, K) // 2, "a"), c.flat(a_sf, _n(M, K) // 16, "a_sf"), c.flat(b, _n(I, K), "b"),
-          c.flat(b_sf, _n(I, K) // 8, "b_sf"), c.flat(alpha, 8, "alpha", 4), c.flat(bias, 4 * _n(I), "bias", 2), act,
-          ph, ldh, M, I, K, c.flat(workspace, 0, "workspace"), _bytes(workspace))
+    (_bind or _native()).gemm_gated(a, a_sf, b, b_sf, alpha, bias, act, h, M, I, K, workspace, stream)
     return h
 
 
@@ -656,11 +606,8 @@ def nvfp4_gemm_gated_quantize(a, a_sf, b, b_sf, alpha, bias, act: int, gs, q, sf
                               workspace=None, stream=None):
     """nvfp4_gemm_gated with h quantised to NVFP4: q uint8 [M][I/2], sf uint8
     [M][I/16], encode scale gs (fp32 [1] or None).  (q, sf) is returned."""
-    c = _Call("nvfp4_gemm_gated_quantize")
-    c.run(stream, c.flat(a, _n(M, K) // 2, "a"), c.flat(a_sf, _n(M, K) // 16, "a_sf"), c.flat(b, _n(I, K), "b"),
-          c.flat(b_sf, _n(I, K) // 8, "b_sf"), c.flat(alpha, 8, "alpha", 4), c.flat(bias, 4 * _n(I), "bias", 2), act,
-          c.flat(gs, 4, "gs", 4), c.flat(q, _n(M, I) // 2, "q"), c.flat(sf, _n(M, I) // 16, "sf"), M, I, K,
-          c.flat(workspace, 0, "workspace"), _bytes(workspace))
+    (_bind or _native()).gemm_gated_quantize(a, a_sf, b, b_sf, alpha, bias, act, gs, q, sf, M, I, K, workspace,
+                                           stream)
     return q, sf
 
 
@@ -669,15 +616,8 @@ def nvfp4_ffn(a, a_sf, w_gu, w_gu_sf, alpha_gu, bias_gu, act: int, gs_h, w_d, w_
     """A dense gated feed-forward on an NVFP4 input [M][H] with an NVFP4 hidden
     layer [M][I]: d = bf16(alpha_d * h W_d^T + bias_d + beta * residual); see
     include/nvfp4.h.  d is returned."""
-    c = _Call("nvfp4_ffn")
-    pr, ldr = c.rows(residual, M, H, "residual")
-    pd, ldd = c.rows(d, M, H, "d")
-    hi = _n(H, I)
-    c.run(stream, c.flat(a, _n(M, H) // 2, "a"), c.flat(a_sf, _n(M, H) // 16, "a_sf"), c.flat(w_gu, hi, "w_gu"),
-          c.flat(w_gu_sf, hi // 8, "w_gu_sf"), c.flat(alpha_gu, 8, "alpha_gu", 4),
-          c.flat(bias_gu, 4 * _n(I), "bias_gu", 2), act, c.flat(gs_h, 4, "gs_h", 4), c.flat(w_d, hi // 2, "w_d"),
-          c.flat(w_d_sf, hi // 16, "w_d_sf"), c.flat(alpha_d, 4, "alpha_d", 4), c.flat(bias_d, 2 * _n(H), "bias_d", 2),
-          pr, ldr, beta, pd, ldd, M, H, I, c.flat(workspace, 0, "workspace"), _bytes(workspace))
+    (_bind or _native()).ffn(a, a_sf, w_gu, w_gu_sf, alpha_gu, bias_gu, act, gs_h, w_d, w_d_sf, alpha_d, bias_d,
+                           residual, beta, d, M, H, I, workspace, stream)
     return d
 
 
@@ -689,14 +629,6 @@ def nvfp4_residual_norm(x, post_weight, post_bias, gate, gate_group: int, residu
     bf16 [H]; gate: bf16 [H] (gate_group 0) or [ceil(T / gate_group)][H]; every
     tensor but x may be None, one output at least is given.  (r, y, q, sf) is
     returned."""
-    c = _Call("nvfp4_residual_norm")
-    gates = 0 if gate_group < 0 else 1 if gate_group == 0 else -(-T // gate_group)
-    px, ldx = c.rows(x, T, H, "x")
-    ps, lds = c.rows(residual, T, H, "residual")
-    pr, ldr = c.rows(r, T, H, "r")
-    py, ldy = c.rows(y, T, H, "y")
-    c.run(stream, px, ldx, c.flat(post_weight, 2 * _n(H), "post_weight", 2), c.flat(post_bias, 2 * _n(H), "post_bias", 2),
-          c.flat(gate, 2 * _n(gates, H), "gate", 2), gate_group, ps, lds, beta, c.flat(weight, 2 * _n(H), "weight", 2),
-          c.flat(bias, 2 * _n(H), "bias", 2), eps, kind, pr, ldr, py, ldy, c.flat(gs, 4, "gs", 4),
-          c.flat(q, _n(T, H) // 2, "q"), c.flat(sf, _n(T, H) // 16, "sf"), T, H)
+    (_bind or _native()).residual_norm(x, post_weight, post_bias, gate, gate_group, residual, beta, weight, bias, eps,
+                                     kind, r, y, gs, q, sf, T, H, stream)
     return r, y, q, sf

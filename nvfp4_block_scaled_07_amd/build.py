@@ -7,7 +7,8 @@ instructions are disabled for all device code.  ``gemm_large.hip`` (the two
 large-M NVFP4 tiles) is compiled to an object of its own, with the iterative
 ILP instruction scheduler, and so is each source of the block operators
 (``csrc/block``), all at the same time as the rest; one last hipcc call links
-them.
+them.  ``csrc/binding.cpp``, the native marshalling of the block operators'
+Python calls, is host code against torch's headers and becomes ``_binding.so``.
 """
 from __future__ import annotations
 
@@ -21,6 +22,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libnvfp4_gfx950.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["api.hip", "gemm.hip", "layout.hip", "moe.hip", "quantize.hip"]
 # sources compiled separately, with extra flags
 SCHED_SOURCES = {"gemm_large.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]}
@@ -60,6 +62,20 @@ def command(out: str = LIB, objdir: str = "") -> list:
     return [HIPCC, *FLAGS, *objs, "-o", out]
 
 
+def binding_command(out: str = BINDING) -> list:
+    """The g++ call that compiles the marshalling module against torch's headers."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(os.path.abspath(torch.__file__))
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", os.path.join(t, "include"), "-isystem", os.path.join(rocm, "include"),
+            "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", out,
+            "-L", os.path.join(t, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+
+
 def _run(cmd: list, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -68,20 +84,22 @@ def _run(cmd: list, verbose: bool) -> None:
     msgs = [l for l in (res.stdout + res.stderr).splitlines()
             if l.strip() and "packed-fp32-ops" not in l and "is not a recognized feature" not in l]
     if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into the in-tree library; returns its path."""
-    tmp = LIB + ".tmp"
+    """Compile every HIP source into the in-tree library, and the marshalling
+    module; returns the library's path."""
+    tmp, btmp = LIB + ".tmp", BINDING + ".tmp"
     with tempfile.TemporaryDirectory(prefix="nvfp4_build_") as objdir:
         with ThreadPoolExecutor(len(os.sched_getaffinity(0))) as pool:
-            for done in [pool.submit(_run, cmd, verbose) for cmd in object_commands(objdir)]:
+            for done in [pool.submit(_run, cmd, verbose) for cmd in [*object_commands(objdir), binding_command(btmp)]]:
                 done.result()
         _run(command(tmp, objdir), verbose)
     os.replace(tmp, LIB)
+    os.replace(btmp, BINDING)
     return LIB
 
 

@@ -1,13 +1,13 @@
 // Epilogues of the block GEMMs: what happens to a tile's fp32 sums between
 // the last MFMA and the one rounding to the output.
 //
-// The MFMA layouts give a lane one column and rows four apart, so its own
-// accumulators touch 2 bytes of a row.  Every epilogue therefore passes the
-// sums through LDS (free by then: the main loop's stages are done) and reads
-// them back with 8 or 16 consecutive columns of one row per lane: bias,
-// residual and output move as 16-byte vectors, a gate column meets its up
-// column in one lane, and a 16-element NVFP4 block belongs to one lane, which
-// quantises it with no cross-lane step.
+// The MFMA layouts give a lane one column and rows four apart.  The unsplit
+// large tiles of the plain epilogue work on that layout (finish_direct: 64
+// bytes of a row per half wave; stores and the next block's residual loads in
+// flight while a block is computed).  Where a sum passes through LDS anyway
+// (K-groups, split K), or a result needs its neighbours (a gate column its up
+// column, an NVFP4 block its 16 columns), the tile is read back from LDS with
+// consecutive columns per lane.
 //
 // Arithmetic is fp32, in the order of the formulas, one rounding per step and
 // one rounding to bf16 (or to e4m3 and e2m1) at the end.  The sums and the
@@ -19,43 +19,82 @@
 
 namespace nvfp4 {
 
-// 1 / (1 + exp(-x)) from the hardware exp2 and reciprocal (1 ulp each).  The
-// argument's rounding adds |x| 2^-24 relative error where the value is small;
-// both stay far below half a bf16 step (2^-9).  exp2 overflows to infinity and
-// the reciprocal gives 0, the limit; NaN stays NaN.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+// Activations (u = 2^-24).  Each is the argument times a factor in (0, 1) built
+// from the hardware exp2 and reciprocal (1 ulp each); the exponent's rounding
+// gives the value a relative error of the exponent's size times u, large only
+// where the value itself vanishes, and far below the bf16 step (2^-8) and the
+// e2m1 step that the result is rounded to.  exp2 overflowing to infinity or
+// underflowing to 0 gives the limits.  NaN stays NaN.
+
+// x / (1 + exp2(e)): x sigmoid(-e ln 2)
+__device__ __forceinline__ float over_one_plus_exp2(float x, float e) {
+  return x * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(e));
 }
 
-__device__ __forceinline__ float activate(float x, int act) {
-  switch (act) {  // uniform
-    case 1: return x < 0.0f ? 0.0f : x;  // NaN stays NaN
-    case 2: return 0.5f * x * erfcf(x * -0.70710678f);
-    // 0.5 x (1 + tanh(z)) = x sigmoid(2 z), z = sqrt(2 / pi) (x + 0.044715 x^3)
-    case 3: return x * sigmoid_f32(1.59576912f * (x + 0.044715f * x * x * x));
-    case 4: return x * sigmoid_f32(x);
-    default: return x;
+// x Phi(x) = max(x, 0) - |x| / 2 erfc(|x| / sqrt 2), which has no cancellation
+// for x < 0.  With z = |x| / sqrt 2 and t = 1 / (1 + z / 2), erfc(z) = t exp2(p(t)
+// - z^2 log2 e); p is a degree-8 Chebyshev fit of log2(erfc(z) exp(z^2) / t)
+// over |x| <= 20 (relative error 6.5 u; erfc is 0 in fp32 beyond).  13 VALU
+// instructions and the two transcendental ones.
+__device__ __forceinline__ float gelu_erf(float x) {
+  const float a = fminf(fabsf(x), 20.0f);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.35355339f, 1.0f));
+  float e = 0.0656675398f;
+  e = __builtin_fmaf(e, t, -0.571985662f);
+  e = __builtin_fmaf(e, t, 1.66417825f);
+  e = __builtin_fmaf(e, t, -2.05382848f);
+  e = __builtin_fmaf(e, t, 0.885032177f);
+  e = __builtin_fmaf(e, t, -0.200422123f);
+  e = __builtin_fmaf(e, t, 0.599930644f);
+  e = __builtin_fmaf(e, t, 1.43694723f);
+  e = __builtin_fmaf(e, t, -1.82552004f);
+  e = __builtin_fmaf(a * a, -0.72134752f, e);
+  return (x < 0.0f ? 0.0f : x) - 0.5f * a * t * __builtin_amdgcn_exp2f(e);
+}
+
+template <int W>
+__device__ __forceinline__ void activate(float (&v)[W], int act) {
+  if (act == 4) {  // uniform branches, once per chunk
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = over_one_plus_exp2(v[i], v[i] * -1.44269504f);
+  } else if (act == 3) {
+    // x (1 + tanh(z)) / 2 = x sigmoid(2 z), z = sqrt(2 / pi) (x + 0.044715 x^3)
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float x = v[i];
+      v[i] = over_one_plus_exp2(x, x * __builtin_fmaf(x * x, -0.102943240f, -2.30220820f));
+    }
+  } else if (act == 2) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = gelu_erf(v[i]);
+  } else if (act == 1) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
   }
 }
 
-// W (a multiple of 8) bf16 values at p, columns [col, cols) valid, as fp32;
-// the others are 0.  vec: p is 16-byte aligned when col is a multiple of 8.
+// 8 bf16 values at p, packed; columns [col, cols) are valid, the others 0.
+// vec: p is 16-byte aligned when col is a multiple of 8.
+__device__ __forceinline__ u4_t load_bf16x8(const uint16_t* p, int64_t col, int64_t cols, bool vec) {
+  if (vec && col + 8 <= cols) return *(const u4_t*)p;
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = col + i < cols ? p[i] : 0u;
+  return u4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+}
+
+__device__ __forceinline__ float bf16_of(u4_t w, int i) {
+  return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+}
+
+// v[i] += the W bf16 values at p (a bias vector)
 template <int W>
-__device__ __forceinline__ void load_bf16(float (&v)[W], const uint16_t* p, int64_t col, int64_t cols, bool vec) {
-  if (vec && col + W <= cols) {
+__device__ __forceinline__ void add_bf16(float (&v)[W], const uint16_t* p, int64_t col, int64_t cols, bool vec) {
 #pragma unroll
-    for (int i = 0; i < W / 8; ++i) {
-      f4_t lo, hi;
-      bf16x8_to_f32(*(const u4_t*)(p + 8 * i), lo, hi);
+  for (int c = 0; c < W / 8; ++c) {
+    const u4_t w = load_bf16x8(p + 8 * c, col + 8 * c, cols, vec);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[8 * i + e] = lo[e];
-        v[8 * i + 4 + e] = hi[e];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = col + i < cols ? __uint_as_float((uint32_t)p[i] << 16) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[8 * c + i] += bf16_of(w, i);
   }
 }
 
@@ -74,40 +113,32 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* p, const float (&v)[8], i
 template <bool QUANT>
 constexpr int kChunk = QUANT ? 16 : 8;
 
+// The residual of columns [col, col + 8) of one row (plain epilogues).
+__device__ __forceinline__ u4_t load_residual(const EpilogueLaunch& p, int64_t row, int64_t col) {
+  return load_bf16x8(p.res + row * p.ldr + col, col, p.cols, p.vec);
+}
+
 // The epilogue of columns [col, col + W) of one row, from the sums s (gate or
-// only) and u (up) of those columns.
+// only) and u (up) of those columns and their residual (if p.res).
 template <bool GATED, bool QUANT>
 __device__ __forceinline__ void finish(const EpilogueLaunch& p, float a0, float a1, int64_t row, int64_t col,
-                                       const float (&s)[kChunk<QUANT>], const float (&u)[kChunk<QUANT>]) {
+                                       const float (&s)[kChunk<QUANT>], const float (&u)[kChunk<QUANT>], u4_t res) {
   constexpr int W = kChunk<QUANT>;
   float v[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] = a0 * s[i];
-  if (p.bias) {
-    float b[W];
-    load_bf16<W>(b, p.bias + col, col, p.cols, p.vec);
-#pragma unroll
-    for (int i = 0; i < W; ++i) v[i] += b[i];
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = activate(v[i], p.act);
+  if (p.bias) add_bf16<W>(v, p.bias + col, col, p.cols, p.vec);
+  activate<W>(v, p.act);
   if constexpr (GATED) {
     float t[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) t[i] = a1 * u[i];
-    if (p.bias) {
-      float b[W];
-      load_bf16<W>(b, p.bias + p.cols + col, col, p.cols, p.vec);
-#pragma unroll
-      for (int i = 0; i < W; ++i) t[i] += b[i];
-    }
+    if (p.bias) add_bf16<W>(t, p.bias + p.cols + col, col, p.cols, p.vec);
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] *= t[i];
   } else if (p.res) {
-    float r[W];
-    load_bf16<W>(r, p.res + row * p.ldr + col, col, p.cols, p.vec);
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] += p.beta * r[i];
+    for (int i = 0; i < W; ++i) v[i] += p.beta * bf16_of(res, i);
   }
   if constexpr (QUANT) {
     // cols % 16 == 0: the block is whole
@@ -133,20 +164,106 @@ __device__ __forceinline__ void lds_chunk(float (&v)[W], const float* src) {
   }
 }
 
+// One output from its sum (gate or only) s and up sum u, its residual and its
+// bias values: the epilogue of the small tiles, where a thread has an output
+// or two and everything but the sums was loaded before the main loop.
+struct Scalars {
+  float a0, a1, bias, bias_up, res;
+};
+
+template <bool GATED>
+__device__ __forceinline__ float finish_one(const EpilogueLaunch& p, const Scalars& c, float s, float u) {
+  float v[1] = {c.a0 * s};
+  if (p.bias) v[0] += c.bias;
+  activate<1>(v, p.act);
+  if constexpr (GATED) {
+    float t = c.a1 * u;
+    if (p.bias) t += c.bias_up;
+    return v[0] * t;
+  }
+  if (p.res) v[0] += p.beta * c.res;
+  return v[0];
+}
+
+template <bool GATED>
+__device__ __forceinline__ Scalars load_scalars(const EpilogueLaunch& p, float a0, float a1, int64_t row, int64_t col,
+                                                bool valid) {
+  Scalars c = {a0, a1, 0.0f, 0.0f, 0.0f};
+  auto at = [&](const uint16_t* q, int64_t i) { return __uint_as_float((uint32_t)q[i] << 16); };
+  if (valid && p.bias) c.bias = at(p.bias, col);
+  if constexpr (GATED) {
+    if (valid && p.bias) c.bias_up = at(p.bias, p.cols + col);
+  } else {
+    if (valid && p.res) c.res = at(p.res, row * p.ldr + col);
+  }
+  return c;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
+}
+// within a quad: lane ^ 1, lane ^ 2; within a row of 16: mirrors of 8 and 16
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+// NVFP4 of a 16-element block held by the 16 lanes of a DPP row, one element
+// each: the quantiser's steps (quantize_block16), the block amax by four DPP
+// maxima.  Every lane of the row must be active.  Returns the scale code;
+// codes: those of the lane's 8 elements (its half of the row).
+__device__ __forceinline__ uint32_t quantize_row16(float x, float gs, uint32_t& codes) {
+  float a = fabsf(x);
+  a = fmaxf(a, __uint_as_float(dpp<kDppXor1>(__float_as_uint(a))));
+  a = fmaxf(a, __uint_as_float(dpp<kDppXor2>(__float_as_uint(a))));
+  a = fmaxf(a, __uint_as_float(dpp<kDppHalfMirror>(__float_as_uint(a))));
+  a = fmaxf(a, __uint_as_float(dpp<kDppMirror>(__float_as_uint(a))));
+  const uint32_t code = e4m3_encode_pos((a / 6.0f) * gs);
+  const float sv = e4m3_value_pos(code);
+  const float v = x * (sv == 0.0f ? 0.0f : gs / sv);
+  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, v, 1.0f, 0) & 15u;
+  w <<= 4 * (threadIdx.x & 7);
+  w |= dpp<kDppXor1>(w);
+  w |= dpp<kDppXor2>(w);
+  codes = w | dpp<kDppHalfMirror>(w);
+  return code;
+}
+
 // Epilogue of a tile whose sums lie in LDS, row-major with stride LD (gated:
-// gate columns, then up columns from UP on), by NT threads.
+// gate columns, then up columns from UP on), by NT threads: 8 or 16 columns
+// a thread, or one at a time (lanes along a row) when rows are not aligned.
 template <bool GATED, bool QUANT, int ROWS, int COLS, int LD, int UP, int NT>
 __device__ __forceinline__ void finish_tile(const EpilogueLaunch& p, const float* tile, float a0, float a1, int64_t m0,
                                             int64_t n0, int rows_valid, int cols_valid) {
   constexpr int W = kChunk<QUANT>, kPerRow = COLS / W;
   static_assert(COLS % W == 0 && LD % 4 == 0 && UP % 4 == 0, "chunks of a row");
+  if (!QUANT && !p.vec) {
+    // single columns, 8 at a time: their loads first, then the arithmetic
+    constexpr int B = 8;
+    for (int x0 = threadIdx.x; x0 < ROWS * COLS; x0 += B * NT) {
+      Scalars c[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int x = x0 + i * NT, row = x / COLS, col = x % COLS;
+        c[i] = load_scalars<GATED>(p, a0, a1, m0 + row, n0 + col, row < rows_valid && col < cols_valid);
+      }
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int x = x0 + i * NT, row = x / COLS, col = x % COLS;
+        if (row < rows_valid && col < cols_valid)
+          p.g.d[(m0 + row) * p.ldd + n0 + col] =
+              f32_to_bf16_bits(finish_one<GATED>(p, c[i], tile[row * LD + col], GATED ? tile[row * LD + UP + col] : 0.0f));
+      }
+    }
+    return;
+  }
   for (int c = threadIdx.x; c < ROWS * kPerRow; c += NT) {
     const int row = c / kPerRow, col = c % kPerRow * W;
     if (row >= rows_valid || col >= cols_valid) continue;
     float s[W], u[W];
     lds_chunk<W>(s, tile + row * LD + col);
     if constexpr (GATED) lds_chunk<W>(u, tile + row * LD + UP + col);
-    finish<GATED, QUANT>(p, a0, a1, m0 + row, n0 + col, s, u);
+    u4_t res = {0u, 0u, 0u, 0u};
+    if (!GATED && p.res) res = load_residual(p, m0 + row, n0 + col);
+    finish<GATED, QUANT>(p, a0, a1, m0 + row, n0 + col, s, u, res);
   }
 }
 

@@ -20,24 +20,40 @@ typedef Cfg<128, 128, 2, 2, 32, 256, 2, 0, 1, 2, 16, 0, 0, 1> GatedTile128;
 typedef KCfg<16, 16, 4, 3, 4> EpiReg16x16;
 typedef KCfg<32, 16, 4, 3, 4> EpiReg32x16;
 typedef KCfg<32, 32, 4, 3, 2> EpiReg32x32;
+typedef KCfg<16, 32, 4, 3, 3> EpiReg16x32;
+typedef KCfg<16, 32, 8, 2, 2> EpiReg16x32k8;
 typedef KCfg<16, 32, 4, 3, 2, 0, 1> GatedReg16x16;  // 16 gate and 16 up columns
+typedef KCfg<16, 64, 4, 2, 2, 0, 1> GatedReg16x32;
 typedef KCfg<32, 32, 4, 3, 2, 0, 1> GatedReg32x16;
 
-// Register-streamed tile with a fused epilogue (small M): the K-groups'
-// partial tiles are summed in wave order, and over the splits in split order,
-// into one fp32 tile in LDS that the epilogue reads.
+// Register-streamed tile with a fused epilogue (small M).  What the epilogue
+// reads besides the sums (alpha, bias, residual) is loaded before the main
+// loop, so that after the K-groups' sum (in wave order, and over the splits
+// in split order) only arithmetic and one store remain.  A thread owns single
+// outputs, 16 consecutive lanes 16 columns of a row: one NVFP4 block.
 template <class C, bool QUANT>
 __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::OCC))) void k_gemm_kreg_epilogue(
     EpilogueLaunch p) {
   __shared__ __attribute__((aligned(16))) float red[C::KS * C::kTileFloats];
-  __shared__ __attribute__((aligned(16))) float tile_sum[C::kTileFloats];
   __shared__ int last_flag;
+  constexpr bool kGated = C::kGated;
   constexpr int kCols = C::kBlkN * 16;  // output columns of the tile
+  constexpr int kOut = C::BM * kCols, kPer = (kOut + C::kThreads - 1) / C::kThreads;
+  static_assert(kCols % 16 == 0, "whole NVFP4 blocks in a row of lanes");
   const int tiles_n = (int)p.g.tiles_n, S = p.g.splits;
   const int L = xcd_remap(blockIdx.x, (int)(p.g.tiles_m * p.g.tiles_n) * S);
   const int tile = L / S, z = L % S;
   const int64_t m0 = (int64_t)(tile / tiles_n) * C::BM, n0 = (int64_t)(tile % tiles_n) * kCols;
   const int rows_a = (int)min<int64_t>(C::BM, p.g.M - m0), rows_b = (int)min<int64_t>(kCols, p.cols - n0);
+  const float a0 = p.g.alpha ? p.g.alpha[0] : 1.0f;
+  const float a1 = kGated && p.g.alpha ? p.g.alpha[1] : 1.0f;
+  const float gs = QUANT && p.gs ? *p.gs : 1.0f;
+  Scalars sc[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int x = threadIdx.x + k * C::kThreads, row = x / kCols, col = x % kCols;
+    sc[k] = load_scalars<kGated>(p, a0, a1, m0 + row, n0 + col, row < rows_a && col < rows_b);
+  }
   Mfma<16>::Acc acc[C::TM][C::TN];
   kreg_accumulate<C, 0>(p.g, m0, n0, rows_a, rows_b, z, S, acc);
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -47,36 +63,49 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
 #pragma unroll
     for (int tn = 0; tn < C::TN; ++tn) *(f4_t*)(mine + ((tm * C::TN + tn) * 64 + lane) * 4) = acc[tm][tn];
   __syncthreads();
-  const rsrc_t part = partial_rsrc(p.g.ws + kCounterBytes / 4 + (int64_t)tile * S * C::kTileFloats, S, C::kTileFloats);
-  for (int x = threadIdx.x; x < C::kTileFloats; x += C::kThreads) {
-    const int row = x / C::BN, col = x % C::BN;
-    const int rr = row & 15, cc = col & 15;
-    const int idx = (((row >> 4) * C::TN + (col >> 4)) * 64 + (rr >> 2) * 16 + cc) * 4 + (rr & 3);
+  // the K-groups' sum of the tile's element (row, col), col < BN
+  auto group_sum = [&](int row, int col) {
+    const int idx = (((row >> 4) * C::TN + (col >> 4)) * 64 + ((row & 15) >> 2) * 16 + (col & 15)) * 4 + (row & 3);
     float sum = 0.f;
 #pragma unroll
     for (int w = 0; w < C::KS; ++w) sum += red[w * C::kTileFloats + idx];
-    if (S > 1) store_coherent(part, (uint32_t)(z * C::kTileFloats + x) * 4, sum);
-    else tile_sum[x] = sum;
-  }
+    return sum;
+  };
+  const rsrc_t part = partial_rsrc(p.g.ws + kCounterBytes / 4 + (int64_t)tile * S * C::kTileFloats, S, C::kTileFloats);
   if (S > 1) {
-    // publish the partial, count arrivals, the last split sums all of them
+    // publish the partial, count arrivals; the last split goes on
+    for (int x = threadIdx.x; x < C::kTileFloats; x += C::kThreads)
+      store_coherent(part, (uint32_t)(z * C::kTileFloats + x) * 4, group_sum(x / C::BN, x % C::BN));
     int* counter = (int*)p.g.ws + tile;
     __builtin_amdgcn_s_waitcnt(0);  // this wave's partial stores are complete
     __syncthreads();
     if (threadIdx.x == 0) last_flag = count_arrival(counter, S);
     __syncthreads();
     if (!last_flag) return;
-    for (int x = threadIdx.x; x < C::kTileFloats; x += C::kThreads) {
-      float sum = 0.f;
-      for (int zz = 0; zz < S; ++zz) sum += load_coherent(part, (uint32_t)(zz * C::kTileFloats + x) * 4);
-      tile_sum[x] = sum;
-    }
     if (threadIdx.x == 0) reset_counter(counter);
   }
-  __syncthreads();
-  const float a0 = p.g.alpha ? p.g.alpha[0] : 1.0f;
-  const float a1 = C::kGated && p.g.alpha ? p.g.alpha[1] : 1.0f;
-  finish_tile<C::kGated, QUANT, C::BM, kCols, C::BN, kCols, C::kThreads>(p, tile_sum, a0, a1, m0, n0, rows_a, rows_b);
+  auto total = [&](int row, int col) {
+    if (S == 1) return group_sum(row, col);
+    float sum = 0.f;
+    for (int zz = 0; zz < S; ++zz) sum += load_coherent(part, (uint32_t)(zz * C::kTileFloats + row * C::BN + col) * 4);
+    return sum;
+  };
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int x = threadIdx.x + k * C::kThreads, row = x / kCols, col = x % kCols;
+    if (x >= kOut) break;  // whole waves
+    const float v = finish_one<kGated>(p, sc[k], total(row, col), kGated ? total(row, kCols + col) : 0.0f);
+    const bool valid = row < rows_a && col < rows_b;
+    if constexpr (QUANT) {
+      uint32_t codes;
+      const uint32_t scale = quantize_row16(v, gs, codes);
+      const int64_t r = m0 + row, c = n0 + col;
+      if (valid && c % 8 == 0) *(uint32_t*)(p.q + r * (p.cols / 2) + c / 2) = codes;
+      if (valid && c % 16 == 0) p.sf[r * (p.cols / 16) + c / 16] = (uint8_t)scale;
+    } else if (valid) {
+      p.g.d[(m0 + row) * p.ldd + n0 + col] = f32_to_bf16_bits(v);
+    }
+  }
 }
 
 template <class C, bool QUANT>
@@ -84,10 +113,41 @@ static void launch_kreg_epilogue(const EpilogueLaunch& p, unsigned grid, hipStre
   hipLaunchKernelGGL((k_gemm_kreg_epilogue<C, QUANT>), dim3(grid), dim3(C::kThreads), 0, stream, p);
 }
 
-// The plain epilogue runs the plain GEMM's plans: the epilogue adds no
-// operand traffic to the main loop.
+// Plan kinds that only the block GEMMs have, numbered past the plain GEMM's.
+static constexpr int kReg16x32 = 32, kReg16x32k8 = 33;
+static const PlanKind kEpi32 = {"kreg16x32", 16, 32, 256, true, true, false, EpiReg16x32::KS, EpiReg16x32::D};
+static const PlanKind kEpi33 = {"kreg16x32k8", 16, 32, 256, true, true, false, EpiReg16x32k8::KS, EpiReg16x32k8::D};
+
+static GemmPlan plan_of(const PlanKind& k, int kind, int64_t M, int64_t cols, int64_t K, int forced_splits, bool gated) {
+  GemmPlan pl;
+  pl.kind = kind;
+  pl.name = k.name;
+  pl.tiles_m = (M + k.bm - 1) / k.bm;
+  pl.tiles_n = (cols + k.bn - 1) / k.bn;
+  pl.group_m = 8;
+  if (!k.splitk || pl.tiles_m * pl.tiles_n > kCounterBytes / 4) forced_splits = 1;
+  PlanKind both = k;  // a gated tile's partials hold both matrices' sums
+  if (gated) both.bn *= 2;
+  plan_splits(pl, both, K, forced_splits);
+  return pl;
+}
+
+// The plain epilogue runs the plain GEMM's plans (the epilogue adds no operand
+// traffic to the main loop), except up to M = 16, where 16 x 32 tiles take the
+// place of 32 x 32 ones, half of whose A rows would be empty: 8 waves with all
+// of up to 16 K units in flight at once while a CU gets one work-group, else 4
+// waves (16 x 6144 x 2048: 6.9 us against 8.1; 1 x 6144 x 2048: 6.4 against 7.4;
+// 16 x 6144 x 16384: 20.6 against 24.6; 16 x 16384 x 6144: 18.1 against 20.4).
 GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K) {
+  int fk = -1, fs = 0;
+  const bool forced = forced_plan(kForceGemm, &fk, &fs);
+  if (forced && fk == kReg16x32) return plan_of(kEpi32, fk, M, N, K, fs, false);
+  if (forced && fk == kReg16x32k8) return plan_of(kEpi33, fk, M, N, K, fs, false);
   GemmPlan pl = choose_plan(M, N, K, kAutoKinds);
+  if (M <= 16 && pl.kind == 12 && !(forced && fk == 12)) {
+    if ((N + 31) / 32 <= kCUs) return plan_of(kEpi33, kReg16x32k8, M, N, K, 0, false);
+    return plan_of(kEpi32, kReg16x32, M, N, K, 0, false);
+  }
   if (pl.kind == 15) {  // never split by the plan's own rule; a forced split is not supported here
     pl.splits = 1;
     pl.workspace = 0;
@@ -102,36 +162,34 @@ static const PlanKind kGated15 = {"gated128x64", 128, 64, 256, false, false, fal
 static const PlanKind kGated9 = {"gated64x32k4", 64, 32, 256, true, false, false, 4};
 static const PlanKind kGated10 = {"gatedreg16x16", 16, 16, 256, true, true, false, GatedReg16x16::KS, GatedReg16x16::D};
 static const PlanKind kGated12 = {"gatedreg32x16", 32, 16, 256, true, true, false, GatedReg32x16::KS, GatedReg32x16::D};
+static const PlanKind kGated32 = {"gatedreg16x32", 16, 32, 256, true, true, false, GatedReg16x32::KS, GatedReg16x32::D};
 
 // The plain GEMM's rules on the tiles of both matrices: register tiles up to
 // M = 128 while they need at most one work-group per CU, 256-row tiles once
 // they fill the CUs twice, 128-row tiles three times, else split 64-row tiles.
+// Up to M = 16 wider matrices take 16 x 32 register tiles (16 x 6144 x 2048
+// outputs: 8.6 us against 11.9 for 32 x 16; 16 x 16384 x 6144: 30.6 against 38).
 GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K) {
   auto tiles = [&](const PlanKind& k) { return ((M + k.bm - 1) / k.bm) * ((I + k.bn - 1) / k.bn); };
   int kind = 9;
   if (M <= 128 && tiles(kGated10) <= kCUs) kind = 10;
+  else if (M <= 16 && tiles(kGated32) <= 4 * kCUs) kind = kReg16x32;
   else if (M <= 128 && tiles(kGated12) <= kCUs) kind = 12;
   else if (M <= 32 && tiles(kGated12) <= 4 * kCUs) kind = 12;
   else if (M > 64 && tiles(kGated14) >= 2 * kCUs) kind = 14;
   else if (M > 64 && tiles(kGated15) >= 3 * kCUs) kind = 15;
-  int fk = -1, forced_splits = 0;
-  if (forced_plan(kForceGemm, &fk, &forced_splits) && (fk == 9 || fk == 10 || fk == 12 || fk == 14 || fk == 15))
-    kind = fk;
-  else
-    forced_splits = 0;
-  const PlanKind& k = kind == 14 ? kGated14 : kind == 15 ? kGated15 : kind == 10 ? kGated10 : kind == 12 ? kGated12
-                                                                                                   : kGated9;
-  GemmPlan pl;
-  pl.kind = kind;
-  pl.name = k.name;
-  pl.tiles_m = (M + k.bm - 1) / k.bm;
-  pl.tiles_n = (I + k.bn - 1) / k.bn;
-  pl.group_m = 8;
-  if (!k.splitk || pl.tiles_m * pl.tiles_n > kCounterBytes / 4) forced_splits = 1;
-  PlanKind both = k;  // partial tiles hold both matrices' sums
-  both.bn *= 2;
-  plan_splits(pl, both, K, forced_splits);
-  return pl;
+  int fk = -1, fs = 0;
+  auto has = [](int k) { return k == 9 || k == 10 || k == 12 || k == 14 || k == 15 || k == kReg16x32; };
+  if (forced_plan(kForceGemm, &fk, &fs) && has(fk)) kind = fk;
+  else fs = 0;
+  switch (kind) {
+    case 10: return plan_of(kGated10, kind, M, I, K, fs, true);
+    case 12: return plan_of(kGated12, kind, M, I, K, fs, true);
+    case 14: return plan_of(kGated14, kind, M, I, K, fs, true);
+    case 15: return plan_of(kGated15, kind, M, I, K, fs, true);
+    case kReg16x32: return plan_of(kGated32, kind, M, I, K, fs, true);
+    default: return plan_of(kGated9, kind, M, I, K, fs, true);
+  }
 }
 
 hipError_t launch_gemm_epilogue(const GemmPlan& pl, EpilogueLaunch p, hipStream_t stream) {
@@ -144,6 +202,8 @@ hipError_t launch_gemm_epilogue(const GemmPlan& pl, EpilogueLaunch p, hipStream_
     case 10: launch_kreg_epilogue<EpiReg16x16, false>(p, grid, stream); break;
     case 11: launch_kreg_epilogue<EpiReg32x16, false>(p, grid, stream); break;
     case 12: launch_kreg_epilogue<EpiReg32x32, false>(p, grid, stream); break;
+    case kReg16x32: launch_kreg_epilogue<EpiReg16x32, false>(p, grid, stream); break;
+    case kReg16x32k8: launch_kreg_epilogue<EpiReg16x32k8, false>(p, grid, stream); break;
     case 14:
     case 16: launch_epilogue_large(pl.kind, p, grid, stream); break;
     case 15: launch_epilogue_tile<EpiTile128, false>(p, grid, stream); break;
@@ -157,6 +217,7 @@ static void launch_gated(const GemmPlan& pl, const EpilogueLaunch& p, unsigned g
   switch (pl.kind) {
     case 10: launch_kreg_epilogue<GatedReg16x16, QUANT>(p, grid, stream); break;
     case 12: launch_kreg_epilogue<GatedReg32x16, QUANT>(p, grid, stream); break;
+    case kReg16x32: launch_kreg_epilogue<GatedReg16x32, QUANT>(p, grid, stream); break;
     case 14: launch_gated_large(p, QUANT, grid, stream); break;
     case 15: launch_epilogue_tile<GatedTile128, QUANT>(p, grid, stream); break;
     default: launch_epilogue_tile<GatedTile64k4, QUANT>(p, grid, stream); break;

@@ -9,8 +9,7 @@
 //
 // One pass over memory: a row's chunks of 8 columns stay in the registers of
 // the threads that own them from the first load to the last store, so x and
-// res are read once and r, y written once; every load (the vectors too) is
-// issued before the first sum.  Bound by HBM for long inputs and by one
+// res are read once and r, y written once.  Bound by HBM for long inputs and by one
 // memory round trip plus the launch for a few rows.
 //
 // Arithmetic: the sums of a row (mean, mean square) and rstd are in fp64 and
@@ -25,38 +24,67 @@
 
 namespace nvfp4 {
 
-// The 8 columns of chunk c of a row as packed bf16; columns past H are 0.
-template <bool VEC>
-__device__ __forceinline__ u4_t load_chunk(const uint16_t* row, int64_t c, int64_t H) {
-  if constexpr (VEC) return c * 8 < H ? ((const u4_t*)row)[c] : u4_t{0u, 0u, 0u, 0u};
-  uint32_t h[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = c * 8 + e < H ? row[c * 8 + e] : 0u;
-  return u4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-}
+// Which columns a thread of a row's TPR threads holds: element e (0..7) of its
+// chunk i.
+//  * kVector: 8 consecutive ones, chunk i TPR + tid, as one 16-byte access
+//    (every base, stride and H a multiple of 8);
+//  * kPlain: the same columns, element by element (NVFP4 output on rows that
+//    are not 16-byte aligned: a block's halves in a lane pair);
+//  * kStrided: one of every TPR columns, so that a 2-byte access of a wave
+//    covers one 128-byte run (anything else: odd H, odd strides).
+enum Access { kVector, kPlain, kStrided };
 
-template <bool VEC>
-__device__ __forceinline__ void store_chunk(uint16_t* row, int64_t c, int64_t H, const float (&v)[8]) {
-  const u4_t w = {f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]),
-                  f32x2_to_bf16x2_bits(v[4], v[5]), f32x2_to_bf16x2_bits(v[6], v[7])};
-  if constexpr (VEC) {
-    if (c * 8 < H) ((u4_t*)row)[c] = w;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c * 8 + e < H) row[c * 8 + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+template <int TPR, int ACC>
+struct Columns {
+  int tid;
+  int64_t H;
+  __device__ __forceinline__ int64_t col(int64_t i, int e) const {
+    return ACC == kStrided ? (i * 8 + e) * TPR + tid : (i * TPR + tid) * 8 + e;
   }
-}
+  __device__ __forceinline__ bool valid(int64_t i, int e) const { return col(i, ACC == kVector ? 0 : e) < H; }
+  // chunk i of a row or vector as packed bf16; columns past H are 0
+  __device__ __forceinline__ u4_t load(const uint16_t* row, int64_t i) const {
+    if constexpr (ACC == kVector) return valid(i, 0) ? *(const u4_t*)(row + col(i, 0)) : u4_t{0u, 0u, 0u, 0u};
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = valid(i, e) ? row[col(i, e)] : 0u;
+    return u4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+  }
+  __device__ __forceinline__ void store(uint16_t* row, int64_t i, const float (&v)[8]) const {
+    const u4_t w = {f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]),
+                    f32x2_to_bf16x2_bits(v[4], v[5]), f32x2_to_bf16x2_bits(v[6], v[7])};
+    if constexpr (ACC == kVector) {
+      if (valid(i, 0)) *(u4_t*)(row + col(i, 0)) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (valid(i, e)) row[col(i, e)] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+};
 
 __device__ __forceinline__ float bf16_at(u4_t w, int e) {
   return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
 }
 
-// Sum over the TPR threads of a row, in a fixed order, to all of them.
+template <int CTRL>
+__device__ __forceinline__ double dpp_add(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// Sum over the TPR threads of a row, in a fixed order, to all of them.  Every
+// step adds a lane's value and its partner's, so all lanes get the same bits.
 template <int TPR>
 __device__ __forceinline__ double row_sum(double v, double* cell) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  v = dpp_add<0xB1>(v);   // lane ^ 1
+  v = dpp_add<0x4E>(v);   // lane ^ 2
+  v = dpp_add<0x141>(v);  // mirror of 8 lanes
+  v = dpp_add<0x140>(v);  // mirror of 16 lanes
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
   if constexpr (TPR > 64) {
     __syncthreads();  // the cells' last readers are done
     if ((threadIdx.x & 63) == 0) cell[threadIdx.x >> 6] = v;
@@ -68,7 +96,7 @@ __device__ __forceinline__ double row_sum(double v, double* cell) {
   return v;
 }
 
-// mean (0 for RMS) and rstd of one row from its sums
+// mean (0 for RMS) and rstd of one row
 struct Stats {
   double mean;
   float rstd;
@@ -85,210 +113,228 @@ __device__ __forceinline__ float normed(float v, const Stats& s, bool layer, flo
   return y;
 }
 
-// Statistics of a row held as V chunks of 8 per thread.
-template <int TPR, int V, bool VEC>
-__device__ __forceinline__ Stats row_stats(const float (&v)[V][8], int tid, const NormLaunch& p, double* cell) {
+// Statistics of a row held as V chunks of 8 per thread (columns past H are 0).
+template <int TPR, int V, int ACC>
+__device__ __forceinline__ Stats row_stats(const float (&v)[V][8], const Columns<TPR, ACC>& at, const NormLaunch& p,
+                                           double* cell) {
   Stats s{0.0, 0.0f};
   if (p.layer) {
     double a = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a += (double)v[i][e];  // columns past H are 0
+      for (int e = 0; e < 8; ++e) a += (double)v[i][e];
     s.mean = row_sum<TPR>(a, cell) / (double)p.H;
   }
   double q = 0.0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int64_t c = (int64_t)i * TPR + tid;
+  for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const double d = (double)v[i][e] - s.mean;
-      if (VEC ? c * 8 < p.H : c * 8 + e < p.H) q = __builtin_fma(d, d, q);
+      if (at.valid(i, e)) q = __builtin_fma(d, d, q);
     }
-  }
   s.rstd = rstd_of(row_sum<TPR>(q, cell), p.H, p.eps);
   return s;
 }
 
-template <int TPR, int V, bool VEC>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_residual_norm(NormLaunch p) {
-  constexpr int WG = TPR < 256 ? 256 : TPR;
-  __shared__ double cell[WG / 64];
-  const int64_t t = (int64_t)blockIdx.x * (WG / TPR) + threadIdx.x / TPR;
+// y of one chunk, to bf16 and NVFP4
+template <int TPR, int ACC>
+__device__ __forceinline__ void store_y(const NormLaunch& p, const Columns<TPR, ACC>& at, int64_t t, int64_t i,
+                                        const float (&y)[8], float gs) {
+  if (p.y) at.store(p.y + t * p.ldy, i, y);
+  if constexpr (ACC != kStrided) {
+    const int64_t c = at.col(i, 0);
+    if (p.q && c < p.H) {
+      // H % 16 == 0: the lanes of a pair hold the two halves of a block
+      uint32_t codes;
+      const uint32_t sf = quantize_half_block16(f4_t{y[0], y[1], y[2], y[3]}, f4_t{y[4], y[5], y[6], y[7]}, gs, codes);
+      *(uint32_t*)(p.q + t * (p.H / 2) + c / 2) = codes;
+      if (c % 16 == 0) p.sf[t * (p.H / 16) + c / 16] = (uint8_t)sf;
+    }
+  }
+}
+
+// The vectors (weights, biases, gate) are loaded where they are used, not with
+// the row: they come from L2, and the registers they would hold cost rows in
+// flight per CU, which are what hides the sums' barriers (16384 x 6144 with
+// both norms and a gate: 164 us against 225 with every load issued first; a
+// single row is not slower either, 3.6 us).
+template <int TPR>
+constexpr int kRowsPerGroup = TPR == 64 ? 4 : 1;  // rows of one work-group
+
+template <int TPR, int V, int ACC>
+__global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(NormLaunch p) {
+  __shared__ double cell[TPR / 64];
+  const int64_t t = (int64_t)blockIdx.x * kRowsPerGroup<TPR> + threadIdx.x / TPR;
   if (t >= p.T) return;  // whole waves: a row has 64 threads, or the work-group
-  const int tid = threadIdx.x % TPR;
-  const int64_t H = p.H;
-  const int64_t gt = p.gate_group > 0 ? t / p.gate_group : 0;
-  u4_t x[V], res[V], pw[V], pb[V], g[V], w[V], b[V];
+  const Columns<TPR, ACC> at{(int)threadIdx.x % TPR, p.H};
+  const uint16_t* gate = p.gate ? p.gate + (p.gate_group > 0 ? t / p.gate_group : 0) * p.H : nullptr;
+  u4_t x[V], res[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int64_t c = (int64_t)i * TPR + tid;
-    x[i] = load_chunk<VEC>(p.x + t * p.ldx, c, H);
-    if (p.res) res[i] = load_chunk<VEC>(p.res + t * p.ldres, c, H);
-    if (p.post_w) pw[i] = load_chunk<VEC>(p.post_w, c, H);
-    if (p.post_b) pb[i] = load_chunk<VEC>(p.post_b, c, H);
-    if (p.gate) g[i] = load_chunk<VEC>(p.gate + gt * H, c, H);
-    if (p.w) w[i] = load_chunk<VEC>(p.w, c, H);
-    if (p.b) b[i] = load_chunk<VEC>(p.b, c, H);
+    x[i] = at.load(p.x + t * p.ldx, i);
+    if (p.res) res[i] = at.load(p.res + t * p.ldres, i);
   }
   float v[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[i][e] = bf16_at(x[i], e);
-  if (p.post_w) {
-    const Stats s = row_stats<TPR, V, VEC>(v, tid, p, cell);
+  Stats s{0.0, 0.0f};
+  if (p.post_w) s = row_stats<TPR, V, ACC>(v, at, p, cell);
+  u4_t pw[V], pb[V], g[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int64_t c = (int64_t)i * TPR + tid;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float u = normed(v[i][e], s, p.layer, bf16_at(pw[i], e), true, p.post_b ? bf16_at(pb[i], e) : 0.0f, p.post_b);
-        v[i][e] = (VEC ? c * 8 < H : c * 8 + e < H) ? u : 0.0f;  // columns past H stay out of the sums
-      }
-    }
+  for (int i = 0; i < V; ++i) {
+    if (p.post_w) pw[i] = at.load(p.post_w, i);
+    if (p.post_b) pb[i] = at.load(p.post_b, i);
+    if (gate) g[i] = at.load(gate, i);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (p.gate) v[i][e] = bf16_at(g[i], e) * v[i][e];
+      if (p.post_w)
+        v[i][e] = normed(v[i][e], s, p.layer, bf16_at(pw[i], e), true, p.post_b ? bf16_at(pb[i], e) : 0.0f, p.post_b);
+      if (gate) v[i][e] = bf16_at(g[i], e) * v[i][e];
       if (p.res) v[i][e] = p.beta * bf16_at(res[i], e) + v[i][e];
+      if (!at.valid(i, e)) v[i][e] = 0.0f;  // stays out of the sums
     }
-  if (p.r) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) store_chunk<VEC>(p.r + t * p.ldr, (int64_t)i * TPR + tid, H, v[i]);
+    if (p.r) at.store(p.r + t * p.ldr, i, v[i]);
   }
   if (!p.y && !p.q) return;
-  const Stats s = row_stats<TPR, V, VEC>(v, tid, p, cell);
+  s = row_stats<TPR, V, ACC>(v, at, p, cell);
+  u4_t w[V], b[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (p.w) w[i] = at.load(p.w, i);
+    if (p.b) b[i] = at.load(p.b, i);
+  }
   const float gs = p.q && p.gs ? *p.gs : 1.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int64_t c = (int64_t)i * TPR + tid;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       v[i][e] = normed(v[i][e], s, p.layer, p.w ? bf16_at(w[i], e) : 1.0f, p.w, p.b ? bf16_at(b[i], e) : 0.0f, p.b);
-    if (p.y) store_chunk<VEC>(p.y + t * p.ldy, c, H, v[i]);
-    if (p.q && c * 8 < H) {
-      // H % 16 == 0: the lanes of a pair hold the two halves of a block
-      uint32_t codes;
-      const uint32_t sf = quantize_half_block16(f4_t{v[i][0], v[i][1], v[i][2], v[i][3]},
-                                                f4_t{v[i][4], v[i][5], v[i][6], v[i][7]}, gs, codes);
-      ((uint32_t*)(p.q + t * (H / 2)))[c] = codes;
-      if ((c & 1) == 0) p.sf[t * (H / 16) + c / 2] = (uint8_t)sf;
-    }
+    store_y(p, at, t, i, v[i], gs);
   }
 }
 
 // Rows too long for the registers: the same steps with the row read again for
 // each sum, one work-group per row.  A thread stores only columns it reads,
 // after its last read of them, so r may be x or res here too.
-template <bool VEC>
+template <int ACC>
 __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
   constexpr int TPR = 1024;
   __shared__ double cell[TPR / 64];
   const int64_t t = blockIdx.x, H = p.H;
-  const int64_t gt = p.gate_group > 0 ? t / p.gate_group : 0;
-  const int tid = threadIdx.x;
-  const int64_t n8 = (H + 7) / 8;
-  Stats sx{0.0, 0.0f};
-  if (p.post_w) {
-    if (p.layer) {
-      double a = 0.0;
-      for (int64_t c = tid; c < n8; c += TPR) {
-        const u4_t x = load_chunk<VEC>(p.x + t * p.ldx, c, H);
-        for (int e = 0; e < 8; ++e) a += (double)bf16_at(x, e);
-      }
-      sx.mean = row_sum<TPR>(a, cell) / (double)H;
-    }
-    double q = 0.0;
-    for (int64_t c = tid; c < n8; c += TPR) {
-      const u4_t x = load_chunk<VEC>(p.x + t * p.ldx, c, H);
-      for (int e = 0; e < 8; ++e) {
-        const double d = (double)bf16_at(x, e) - sx.mean;
-        if (c * 8 + e < H) q = __builtin_fma(d, d, q);
-      }
-    }
-    sx.rstd = rstd_of(row_sum<TPR>(q, cell), H, p.eps);
-  }
-  auto r_chunk = [&](int64_t c, float (&v)[8]) {
+  const Columns<TPR, ACC> at{(int)threadIdx.x, H};
+  const uint16_t* gate = p.gate ? p.gate + (p.gate_group > 0 ? t / p.gate_group : 0) * H : nullptr;
+  const int64_t n = (H + 8 * TPR - 1) / (8 * TPR);
+  Stats sx{0.0, 0.0f}, sr{0.0, 0.0f};
+  auto x_chunk = [&](int64_t i, float (&v)[8]) {
+    const u4_t x = at.load(p.x + t * p.ldx, i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = bf16_at(x, e);
+  };
+  auto r_chunk = [&](int64_t i, float (&v)[8]) {
     const u4_t none = {0u, 0u, 0u, 0u};
-    const u4_t x = load_chunk<VEC>(p.x + t * p.ldx, c, H);
-    const u4_t res = p.res ? load_chunk<VEC>(p.res + t * p.ldres, c, H) : none;
-    const u4_t pw = p.post_w ? load_chunk<VEC>(p.post_w, c, H) : none, pb = p.post_b ? load_chunk<VEC>(p.post_b, c, H) : none;
-    const u4_t g = p.gate ? load_chunk<VEC>(p.gate + gt * H, c, H) : none;
+    const u4_t res = p.res ? at.load(p.res + t * p.ldres, i) : none;
+    const u4_t pw = p.post_w ? at.load(p.post_w, i) : none, pb = p.post_b ? at.load(p.post_b, i) : none;
+    const u4_t g = gate ? at.load(gate, i) : none;
+    x_chunk(i, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      v[e] = bf16_at(x, e);
       if (p.post_w) v[e] = normed(v[e], sx, p.layer, bf16_at(pw, e), true, bf16_at(pb, e), p.post_b);
-      if (p.gate) v[e] = bf16_at(g, e) * v[e];
+      if (gate) v[e] = bf16_at(g, e) * v[e];
       if (p.res) v[e] = p.beta * bf16_at(res, e) + v[e];
     }
   };
-  Stats s{0.0, 0.0f};
-  const bool norm = p.y || p.q;
-  if (norm && p.layer) {
-    double a = 0.0;
-    for (int64_t c = tid; c < n8; c += TPR) {
-      float v[8];
-      r_chunk(c, v);
-      for (int e = 0; e < 8; ++e)
-        if (c * 8 + e < H) a += (double)v[e];
+  auto stats = [&](auto&& chunk) {
+    Stats s{0.0, 0.0f};
+    float v[8];
+    if (p.layer) {
+      double a = 0.0;
+      for (int64_t i = 0; i < n; ++i) {
+        chunk(i, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (at.valid(i, e)) a += (double)v[e];
+      }
+      s.mean = row_sum<TPR>(a, cell) / (double)H;
     }
-    s.mean = row_sum<TPR>(a, cell) / (double)H;
-  }
-  if (norm) {
     double q = 0.0;
-    for (int64_t c = tid; c < n8; c += TPR) {
-      float v[8];
-      r_chunk(c, v);
+    for (int64_t i = 0; i < n; ++i) {
+      chunk(i, v);
+#pragma unroll
       for (int e = 0; e < 8; ++e) {
         const double d = (double)v[e] - s.mean;
-        if (c * 8 + e < H) q = __builtin_fma(d, d, q);
+        if (at.valid(i, e)) q = __builtin_fma(d, d, q);
       }
     }
     s.rstd = rstd_of(row_sum<TPR>(q, cell), H, p.eps);
-  }
+    return s;
+  };
+  const bool norm = p.y || p.q;
+  if (p.post_w) sx = stats(x_chunk);
+  if (norm) sr = stats(r_chunk);
   const float gs = p.q && p.gs ? *p.gs : 1.0f;
-  for (int64_t c = tid; c < n8; c += TPR) {
+  for (int64_t i = 0; i < n; ++i) {
     float v[8];
-    r_chunk(c, v);
-    if (p.r) store_chunk<VEC>(p.r + t * p.ldr, c, H, v);
+    r_chunk(i, v);
+    if (p.r) at.store(p.r + t * p.ldr, i, v);
     if (!norm) continue;
     const u4_t none = {0u, 0u, 0u, 0u};
-    const u4_t w = p.w ? load_chunk<VEC>(p.w, c, H) : none, b = p.b ? load_chunk<VEC>(p.b, c, H) : none;
+    const u4_t w = p.w ? at.load(p.w, i) : none, b = p.b ? at.load(p.b, i) : none;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = normed(v[e], s, p.layer, bf16_at(w, e), p.w, bf16_at(b, e), p.b);
-    if (p.y) store_chunk<VEC>(p.y + t * p.ldy, c, H, v);
-    if (p.q) {
-      uint32_t codes;
-      const uint32_t sf = quantize_half_block16(f4_t{v[0], v[1], v[2], v[3]}, f4_t{v[4], v[5], v[6], v[7]}, gs, codes);
-      ((uint32_t*)(p.q + t * (H / 2)))[c] = codes;
-      if ((c & 1) == 0) p.sf[t * (H / 16) + c / 2] = (uint8_t)sf;
-    }
+    for (int e = 0; e < 8; ++e) v[e] = normed(v[e], sr, p.layer, bf16_at(w, e), p.w, bf16_at(b, e), p.b);
+    store_y(p, at, t, i, v, gs);
   }
 }
 
 template <int TPR, int V>
 static void launch_norm(const NormLaunch& p, hipStream_t stream) {
-  constexpr int WG = TPR < 256 ? 256 : TPR, kRows = WG / TPR;
-  const unsigned grid = (unsigned)((p.T + kRows - 1) / kRows);
-  if (p.vec) hipLaunchKernelGGL((k_residual_norm<TPR, V, true>), dim3(grid), dim3(WG), 0, stream, p);
-  else hipLaunchKernelGGL((k_residual_norm<TPR, V, false>), dim3(grid), dim3(WG), 0, stream, p);
+  constexpr int R = kRowsPerGroup<TPR>;
+  const dim3 grid((unsigned)((p.T + R - 1) / R)), block(TPR * R);
+  if (p.vec) hipLaunchKernelGGL((k_residual_norm<TPR, V, kVector>), grid, block, 0, stream, p);
+  else if (p.q) hipLaunchKernelGGL((k_residual_norm<TPR, V, kPlain>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((k_residual_norm<TPR, V, kStrided>), grid, block, 0, stream, p);
 }
 
+static void launch_norm_long(const NormLaunch& p, hipStream_t stream) {
+  const dim3 grid((unsigned)p.T), block(1024);
+  if (p.vec) hipLaunchKernelGGL((k_residual_norm_long<kVector>), grid, block, 0, stream, p);
+  else if (p.q) hipLaunchKernelGGL((k_residual_norm_long<kPlain>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((k_residual_norm_long<kStrided>), grid, block, 0, stream, p);
+}
+
+// Threads per row and chunks per thread.  Up to two rows per CU a call is one
+// row's latency: a chunk a thread while a work-group can hold the row (6144
+// columns: 768 x 1 3.65 us against 4.29 for 256 x 3; 2048: 2.8 against 3.4 for
+// 128 x 2).  With more rows, few threads a row: more rows in flight per CU
+// between the barriers of the sums (16276 rows of 6144, both norms and a gate:
+// 256 x 3 162 us, 384 x 2 241, 768 x 1 224; 4096 rows of 12288: 256 x 6 100 us,
+// 512 x 3 117, 1024 x 2 135; a wave a row, 64 x 12, holds too few waves: 354).
 hipError_t launch_residual_norm(const NormLaunch& p, hipStream_t stream) {
   const int64_t n8 = (p.H + 7) / 8;
-  if (n8 <= 64) launch_norm<64, 1>(p, stream);
-  else if (n8 <= 128) launch_norm<64, 2>(p, stream);
-  else if (n8 <= 256) launch_norm<256, 1>(p, stream);
-  else if (n8 <= 512) launch_norm<256, 2>(p, stream);
-  else if (n8 <= 768) launch_norm<256, 3>(p, stream);
-  else if (n8 <= 1024) launch_norm<512, 2>(p, stream);
-  else if (n8 <= 2048) launch_norm<1024, 2>(p, stream);
-  else if (p.vec) hipLaunchKernelGGL((k_residual_norm_long<true>), dim3((unsigned)p.T), dim3(1024), 0, stream, p);
-  else hipLaunchKernelGGL((k_residual_norm_long<false>), dim3((unsigned)p.T), dim3(1024), 0, stream, p);
+  if (n8 > 2048) launch_norm_long(p, stream);
+  else if (n8 > 1536) launch_norm<1024, 2>(p, stream);
+  else if (n8 <= 64) launch_norm<64, 1>(p, stream);
+  else if (p.T <= 2 * kCUs) {
+    if (n8 <= 128) launch_norm<128, 1>(p, stream);
+    else if (n8 <= 256) launch_norm<256, 1>(p, stream);
+    else if (n8 <= 512) launch_norm<512, 1>(p, stream);
+    else if (n8 <= 768) launch_norm<768, 1>(p, stream);
+    else if (n8 <= 1024) launch_norm<512, 2>(p, stream);
+    else launch_norm<768, 2>(p, stream);
+  } else {
+    if (n8 <= 128) launch_norm<64, 2>(p, stream);
+    else if (n8 <= 256) launch_norm<128, 2>(p, stream);
+    else if (n8 <= 512) launch_norm<256, 2>(p, stream);
+    else if (n8 <= 768) launch_norm<256, 3>(p, stream);
+    else if (n8 <= 1024) launch_norm<256, 4>(p, stream);
+    else launch_norm<256, 6>(p, stream);
+  }
   return hipGetLastError();
 }
 

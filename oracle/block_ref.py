@@ -13,10 +13,12 @@ bound that the kernel's roundings allow, term by term (u = 2^-24):
   fp32 summation that ``nvfp4_ref.gemm_tolerance`` uses;
 * alpha s, + bias, * beta, + residual, the gated product: u of the value each;
 * an activation: its slope (at most 1.13) times the error of its argument, plus
-  its own evaluation error, at most (4 |x| + 16) u of the value for x times a
-  sigmoid of a cubic or linear argument (the argument's relative rounding
-  scales with its size, which the exponential turns into a relative error of
-  the value; exp2 and reciprocal are within an ulp each), and as much for erf;
+  its own evaluation error, at most (16 + 4 E) u of the value, where E is the
+  size of the exponential's argument (|x| for SiLU, 2 sqrt(2 / pi) (|x| +
+  0.044715 |x|^3) for the tanh form, x^2 / 2 for the erf form): an argument
+  made of at most 4 roundings is off by 4 E u, which the exponential turns into
+  a relative error of its value; 16 u cover the polynomial of the erf form (its
+  fit and 9 steps), exp2 and reciprocal (2 u each) and the remaining products;
 * the output: half a bf16 step, 2^-8 of the value at most.
 
 The norm's arithmetic is fixed step by step (fp64 sums, fp32 elsewhere), so
@@ -33,7 +35,6 @@ from oracle import nvfp4_ref as o
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 RMS, LAYER = 0, 1
 U = 2.0 ** -24
-_erf = np.vectorize(math.erf, otypes=[np.float64])
 _erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
@@ -56,7 +57,9 @@ def _act_error(x, y, act, dx):
     """Bound of the fp32 activation's error for an argument off by dx."""
     if act in (ACT_NONE, ACT_RELU):
         return dx
-    return 1.13 * dx + (4.0 * np.abs(x) + 16.0) * U * np.abs(y) + 2.0 ** -126
+    a = np.abs(x)
+    e = {ACT_SILU: a, ACT_GELU: a * a / 2, ACT_GELU_TANH: 1.6 * a + 0.0714 * a ** 3}[act]
+    return 1.13 * dx + (16.0 + 4.0 * e) * U * np.abs(y) + 2.0 ** -126
 
 
 def _sum_and_error(xa, xb, alpha, bias):

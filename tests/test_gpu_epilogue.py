@@ -40,7 +40,7 @@ def _check(M, N, K, seed, act=nv.ACT_NONE, bias=False, residual=False, beta=1.0,
 
 
 # one shape per plan family, each odd in M or N where the family allows
-SHAPES = [(1, 768, 512), (16, 768, 6144), (5, 33, 256), (31, 4096, 512), (64, 2048, 1024), (128, 4096, 512),
+SHAPES = [(1, 768, 512), (1, 6144, 2048), (16, 9000, 512), (16, 768, 6144), (5, 33, 256), (31, 4096, 512), (64, 2048, 1024), (128, 4096, 512),
           (61, 777, 1280), (200, 300, 768), (513, 1025, 512)]
 
 
@@ -57,7 +57,7 @@ def test_activations_bias_and_residual(act, bias, residual):
 
 
 @pytest.mark.parametrize("kind,splits", [(9, 0), (9, 3), (10, 0), (10, 2), (11, 0), (11, 2), (12, 0), (12, 3), (14, 0),
-                                         (15, 0), (15, 4), (16, 0), (3, 2)])
+                                         (15, 0), (15, 4), (16, 0), (3, 2), (32, 0), (32, 2), (33, 0), (33, 3)])
 @pytest.mark.parametrize("M,N,K", [(70, 270, 1536), (257, 195, 768)])
 def test_every_plan_forced(kind, splits, M, N, K, force_plan):
     force_plan(nv.FAMILY_GEMM, kind, splits)

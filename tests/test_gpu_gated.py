@@ -49,7 +49,7 @@ def _check(M, I, K, seed, act=nv.ACT_SILU, bias=False, label=""):
         br.check_quantized(host(q), host(sf), y, err, gs, f"{M}x{I}x{K}")
 
 
-@pytest.mark.parametrize("M,I,K", [(1, 2048, 512), (1, 16, 256), (16, 2048, 6144), (5, 33, 256), (31, 4096, 512),
+@pytest.mark.parametrize("M,I,K", [(1, 2048, 512), (1, 16, 256), (1, 4112, 256), (16, 9008, 512), (16, 2048, 6144), (5, 33, 256), (31, 4096, 512),
                                    (64, 2048, 1024), (128, 4096, 512), (100, 784, 1280), (333, 1001, 1536),
                                    (513, 1040, 512)])
 @pytest.mark.parametrize("bias", [False, True])
@@ -63,7 +63,7 @@ def test_activations(act):
 
 
 @pytest.mark.parametrize("kind,splits", [(9, 0), (9, 3), (10, 0), (10, 2), (12, 0), (12, 3), (14, 0), (15, 0), (15, 4),
-                                         (16, 0)])
+                                         (16, 0), (32, 0), (32, 2)])
 @pytest.mark.parametrize("M,I,K", [(70, 272, 1536), (257, 99, 768)])
 def test_every_plan_forced(kind, splits, M, I, K, force_plan):
     force_plan(nv.FAMILY_GEMM, kind, splits)

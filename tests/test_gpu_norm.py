@@ -86,6 +86,13 @@ def test_lengths(H, kind):
     _check(5, H, H + kind, kind, True, None, True)
 
 
+@pytest.mark.parametrize("H", [16, 1000, 1024, 1545, 2064, 4096, 6144, 6145, 8208, 12288, 12289, 16384])
+@pytest.mark.parametrize("kind", [nv.NORM_RMS, nv.NORM_LAYER])
+def test_many_rows(H, kind):
+    # past two rows per CU the rows take fewer threads each
+    _check(515, H, H + 7 * kind, kind, True, 100, True)
+
+
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 37, 300])
 @pytest.mark.parametrize("H", [96, 768, 6144])
 def test_rows(T, H):
