@@ -445,10 +445,9 @@ nvfp4_status nvfp4_force_plan(int32_t family, int32_t kind, int32_t splits);
  * workspaces are as for nvfp4_gemm; sums and every step of an epilogue are
  * fp32 and the result is rounded once.
  *
- * Row strides (ld*) count elements; a stride of 0 means the row length.  Rows
- * are accessed 16 bytes at a time when the bases are 16-byte aligned and the
- * strides multiples of 8, else element by element (2-byte alignment is all
- * that bf16 arguments need here).
+ * Row strides (ld*) count elements; a stride of 0 means the row length.  bf16
+ * arguments need 2-byte alignment only (rows are accessed 16 bytes at a time
+ * at any alignment; 16-byte aligned ones cost a few per cent less).
  */
 typedef enum {
   NVFP4_ACT_NONE = 0,
@@ -469,8 +468,8 @@ typedef enum {
  * workspace: nvfp4_gemm_epilogue_workspace_size(M, N, K) bytes, under the
  * rules of nvfp4_gemm (zero-filled once, calls sharing it ordered on one
  * stream: two captured graphs that share it must not run at the same time).
- * ERR_SHAPE for an unknown act or a stride below N; ERR_UNSUPPORTED when the
- * output has 2^31 tiles or more.
+ * ERR_SHAPE for an unknown act or a stride below N; ERR_UNSUPPORTED when M N is
+ * past 2^35 (M rounded up to 16, N to 16).
  */
 nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
                                  const float* alpha, const uint16_t* bias, int32_t act, const uint16_t* residual,
@@ -548,8 +547,8 @@ size_t nvfp4_ffn_workspace_size(int64_t M, int64_t H, int64_t I);
  * may be x or residual (same pointer and stride); outputs must not otherwise
  * overlap inputs or each other.  ldx, ldres, ldr, ldy: row strides of x,
  * residual, r and y.  y is computed from the unrounded r.  Sums over a row and
- * rstd are fp64, rounded once to fp32; the other steps fp32.  Any H >= 1; T ==
- * 0 is a successful no-op.  No workspace.
+ * rstd are fp64, rounded once to fp32; the other steps fp32.  Any H from 1
+ * to 2^30; T == 0 is a successful no-op.  No workspace.
  */
 typedef enum { NVFP4_NORM_RMS = 0, NVFP4_NORM_LAYER = 1 } nvfp4_norm_kind;
 nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t* post_weight,

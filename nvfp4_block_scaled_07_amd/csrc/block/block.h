@@ -20,7 +20,6 @@ struct EpilogueLaunch {
   int64_t cols;          // output columns: N, or I
   float beta;
   int act;
-  int vec;  // 16-byte accesses of bias, res and d are aligned at every column multiple of 8
   const float* gs;
   uint8_t* q;
   uint8_t* sf;
@@ -54,8 +53,8 @@ struct NormLaunch {
   int64_t ldx, ldres, ldr, ldy;  // row strides in elements
   int64_t gate_group;            // rows that share a gate row; 0: all of them
   float beta, eps;
+  double inv_h;                  // 1 / H
   int layer;                     // 0: RMS, 1: mean removed first
-  int vec;                       // every row and vector is 16-byte aligned and H % 8 == 0
 };
 hipError_t launch_residual_norm(const NormLaunch& p, hipStream_t stream);
 

@@ -22,11 +22,8 @@ bool stride_ok(int64_t* ld, int64_t cols) {
   return *ld >= cols;
 }
 
-// 16-byte vectors at every column multiple of 8
-bool vec16(const void* p, int64_t ld) { return !p || (aligned(p, 16) && ld % 8 == 0); }
-
-// Sizes whose tiles and work-groups can be counted in 31 bits, and whose
-// output rows can be addressed: the smallest tile has 16 x 16 outputs.
+// M N <= 2^35: tiles (16 x 16 outputs at least) times splits (16 at most) can
+// be counted in 31 bits.
 bool sizes_ok(int64_t M, int64_t N) {
   const int64_t kMax = int64_t(1) << 40;
   if (M > kMax || N > kMax) return false;
@@ -54,7 +51,7 @@ nvfp4_status check_gemm(const char* fn, const void* a, const void* a_sf, const v
   if (!aligned(alpha, 4) || !aligned(bias, 2))
     return fail(NVFP4_ERR_ALIGN, "%s: alpha must be 4-byte and bias 2-byte aligned", fn);
   if (!sizes_ok(M, cols))
-    return fail(NVFP4_ERR_UNSUPPORTED, "%s: %lld x %lld outputs are 2^31 tiles or more", fn, (long long)M, (long long)cols);
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: %lld x %lld outputs: at most 2^35 are supported", fn, (long long)M, (long long)cols);
   return NVFP4_OK;
 }
 
@@ -106,7 +103,6 @@ hipError_t run_epilogue(const GemmPlan& plan, EpilogueLaunch p, const uint16_t* 
   p.beta = beta;
   p.g.d = d;
   p.ldd = ldd;
-  p.vec = vec16(p.bias, 8) && vec16(residual, ldr) && vec16(d, ldd);
   return nvfp4::launch_gemm_epilogue(plan, p, stream);
 }
 
@@ -159,7 +155,6 @@ nvfp4_status nvfp4_gemm_gated(const uint8_t* a, const uint8_t* a_sf, const uint8
   EpilogueLaunch p = launch_of(a, a_sf, b, b_sf, alpha, bias, act, M, 2 * I, I, K, workspace);
   p.g.d = h;
   p.ldd = ldh;
-  p.vec = vec16(bias, I) && vec16(h, ldh);
   return hip_status(nvfp4::launch_gemm_gated(plan, p, false, (hipStream_t)stream), fn);
 }
 
@@ -180,7 +175,6 @@ nvfp4_status nvfp4_gemm_gated_quantize(const uint8_t* a, const uint8_t* a_sf, co
   p.gs = gs;
   p.q = q;
   p.sf = sf;
-  p.vec = vec16(bias, I);
   return hip_status(nvfp4::launch_gemm_gated(plan, p, true, (hipStream_t)stream), fn);
 }
 
@@ -237,7 +231,6 @@ nvfp4_status nvfp4_ffn(const uint8_t* a, const uint8_t* a_sf, const uint8_t* w_g
   p.gs = gs_h;
   p.q = base + f.codes;
   p.sf = base + f.scales;
-  p.vec = vec16(bias_gu, I);
   const hipError_t e = nvfp4::launch_gemm_gated(f.gated, p, true, (hipStream_t)stream);
   if (e != hipSuccess) return hip_status(e, fn);
   p = launch_of(base + f.codes, base + f.scales, w_d, w_d_sf, alpha_d, bias_d, NVFP4_ACT_NONE, M, H, H, I, workspace);
@@ -260,8 +253,8 @@ nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t*
     return fail(NVFP4_ERR_SHAPE, "%s: H = %lld is not a multiple of the block size 16", fn, (long long)H);
   if (!stride_ok(&ldx, H) || !stride_ok(&ldres, H) || !stride_ok(&ldr, H) || !stride_ok(&ldy, H))
     return fail(NVFP4_ERR_SHAPE, "%s: a row stride is below H = %lld", fn, (long long)H);
-  if (T > INT32_MAX || H > (int64_t(1) << 40))
-    return fail(NVFP4_ERR_UNSUPPORTED, "%s: T = %lld rows, H = %lld: at most 2^31 - 1 rows of 2^40", fn, (long long)T, (long long)H);
+  if (T > INT32_MAX || H > (int64_t(1) << 30))
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: T = %lld rows, H = %lld: at most 2^31 - 1 rows of 2^30", fn, (long long)T, (long long)H);
   if (T == 0) return ok();
   if (!x) return fail(NVFP4_ERR_NULL, "%s: x must not be NULL", fn);
   if (!r && !y && !q) return fail(NVFP4_ERR_NULL, "%s: no output: r, y and q are all NULL", fn);
@@ -293,8 +286,7 @@ nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t*
   p.gate_group = gate_group;
   p.beta = beta;
   p.eps = eps;
+  p.inv_h = 1.0 / (double)H;
   p.layer = kind == NVFP4_NORM_LAYER;
-  p.vec = H % 8 == 0 && vec16(x, ldx) && vec16(residual, ldres) && vec16(r, ldr) && vec16(y, ldy) &&
-          vec16(post_weight, H) && vec16(post_bias, H) && vec16(gate, H) && vec16(weight, H) && vec16(bias, H);
   return hip_status(nvfp4::launch_residual_norm(p, (hipStream_t)stream), fn);
 }

@@ -16,6 +16,7 @@
 
 #include "../kreg_tile.h"
 #include "block.h"
+#include "vec8.h"
 
 namespace nvfp4 {
 
@@ -74,39 +75,24 @@ __device__ __forceinline__ void activate(float (&v)[W], int act) {
 }
 
 // 8 bf16 values at p, packed; columns [col, cols) are valid, the others 0.
-// vec: p is 16-byte aligned when col is a multiple of 8.
-__device__ __forceinline__ u4_t load_bf16x8(const uint16_t* p, int64_t col, int64_t cols, bool vec) {
-  if (vec && col + 8 <= cols) return *(const u4_t*)p;
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = col + i < cols ? p[i] : 0u;
-  return u4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-}
-
-__device__ __forceinline__ float bf16_of(u4_t w, int i) {
-  return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+__device__ __forceinline__ u4_t load_bf16x8(const uint16_t* p, int64_t col, int64_t cols) {
+  return col + 8 <= cols ? load8(p) : load_tail8(p, (int)(cols & 7));
 }
 
 // v[i] += the W bf16 values at p (a bias vector)
 template <int W>
-__device__ __forceinline__ void add_bf16(float (&v)[W], const uint16_t* p, int64_t col, int64_t cols, bool vec) {
+__device__ __forceinline__ void add_bf16(float (&v)[W], const uint16_t* p, int64_t col, int64_t cols) {
 #pragma unroll
   for (int c = 0; c < W / 8; ++c) {
-    const u4_t w = load_bf16x8(p + 8 * c, col + 8 * c, cols, vec);
+    const u4_t w = load_bf16x8(p + 8 * c, col + 8 * c, cols);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[8 * c + i] += bf16_of(w, i);
+    for (int i = 0; i < 8; ++i) v[8 * c + i] += bf16_at(w, i);
   }
 }
 
-__device__ __forceinline__ void store_bf16x8(uint16_t* p, const float (&v)[8], int64_t col, int64_t cols, bool vec) {
-  if (vec && col + 8 <= cols) {
-    *(u4_t*)p = u4_t{f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]),
-                     f32x2_to_bf16x2_bits(v[4], v[5]), f32x2_to_bf16x2_bits(v[6], v[7])};
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < cols) p[i] = f32_to_bf16_bits(v[i]);
-  }
+__device__ __forceinline__ void store_bf16x8(uint16_t* p, const float (&v)[8], int64_t col, int64_t cols) {
+  if (col + 8 <= cols) store8(p, to_bf16x8(v));
+  else store_tail8(p, to_bf16x8(v), (int)(cols & 7));
 }
 
 // Columns a lane takes at once: one 16-byte bf16 vector, or one NVFP4 block.
@@ -115,7 +101,7 @@ constexpr int kChunk = QUANT ? 16 : 8;
 
 // The residual of columns [col, col + 8) of one row (plain epilogues).
 __device__ __forceinline__ u4_t load_residual(const EpilogueLaunch& p, int64_t row, int64_t col) {
-  return load_bf16x8(p.res + row * p.ldr + col, col, p.cols, p.vec);
+  return load_bf16x8(p.res + row * p.ldr + col, col, p.cols);
 }
 
 // The epilogue of columns [col, col + W) of one row, from the sums s (gate or
@@ -127,18 +113,18 @@ __device__ __forceinline__ void finish(const EpilogueLaunch& p, float a0, float 
   float v[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] = a0 * s[i];
-  if (p.bias) add_bf16<W>(v, p.bias + col, col, p.cols, p.vec);
+  if (p.bias) add_bf16<W>(v, p.bias + col, col, p.cols);
   activate<W>(v, p.act);
   if constexpr (GATED) {
     float t[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) t[i] = a1 * u[i];
-    if (p.bias) add_bf16<W>(t, p.bias + p.cols + col, col, p.cols, p.vec);
+    if (p.bias) add_bf16<W>(t, p.bias + p.cols + col, col, p.cols);
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] *= t[i];
   } else if (p.res) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] += p.beta * bf16_of(res, i);
+    for (int i = 0; i < W; ++i) v[i] += p.beta * bf16_at(res, i);
   }
   if constexpr (QUANT) {
     // cols % 16 == 0: the block is whole
@@ -150,7 +136,7 @@ __device__ __forceinline__ void finish(const EpilogueLaunch& p, float a0, float 
     *(u2_t*)(p.q + row * (p.cols / 2) + col / 2) = u2_t{w[0], w[1]};
     p.sf[row * (p.cols / 16) + col / 16] = (uint8_t)code;
   } else {
-    store_bf16x8(p.g.d + row * p.ldd + col, v, col, p.cols, p.vec);
+    store_bf16x8(p.g.d + row * p.ldd + col, v, col, p.cols);
   }
 }
 
@@ -228,33 +214,13 @@ __device__ __forceinline__ uint32_t quantize_row16(float x, float gs, uint32_t& 
 }
 
 // Epilogue of a tile whose sums lie in LDS, row-major with stride LD (gated:
-// gate columns, then up columns from UP on), by NT threads: 8 or 16 columns
-// a thread, or one at a time (lanes along a row) when rows are not aligned.
+// gate columns, then up columns from UP on), by NT threads, 8 or 16 columns
+// at a time.
 template <bool GATED, bool QUANT, int ROWS, int COLS, int LD, int UP, int NT>
 __device__ __forceinline__ void finish_tile(const EpilogueLaunch& p, const float* tile, float a0, float a1, int64_t m0,
                                             int64_t n0, int rows_valid, int cols_valid) {
   constexpr int W = kChunk<QUANT>, kPerRow = COLS / W;
   static_assert(COLS % W == 0 && LD % 4 == 0 && UP % 4 == 0, "chunks of a row");
-  if (!QUANT && !p.vec) {
-    // single columns, 8 at a time: their loads first, then the arithmetic
-    constexpr int B = 8;
-    for (int x0 = threadIdx.x; x0 < ROWS * COLS; x0 += B * NT) {
-      Scalars c[B];
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int x = x0 + i * NT, row = x / COLS, col = x % COLS;
-        c[i] = load_scalars<GATED>(p, a0, a1, m0 + row, n0 + col, row < rows_valid && col < cols_valid);
-      }
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int x = x0 + i * NT, row = x / COLS, col = x % COLS;
-        if (row < rows_valid && col < cols_valid)
-          p.g.d[(m0 + row) * p.ldd + n0 + col] =
-              f32_to_bf16_bits(finish_one<GATED>(p, c[i], tile[row * LD + col], GATED ? tile[row * LD + UP + col] : 0.0f));
-      }
-    }
-    return;
-  }
   for (int c = threadIdx.x; c < ROWS * kPerRow; c += NT) {
     const int row = c / kPerRow, col = c % kPerRow * W;
     if (row >= rows_valid || col >= cols_valid) continue;

@@ -19,53 +19,46 @@
 // the second norm).  Built without fp contraction, so a plain evaluation of
 // the same steps gives the same bits, the NVFP4 codes and scales among them.
 // The fp64 sums cost two instructions an element, far below the memory time.
-#include "../device.h"
 #include "block.h"
+#include "vec8.h"
 
 namespace nvfp4 {
 
-// Which columns a thread of a row's TPR threads holds: element e (0..7) of its
-// chunk i.
-//  * kVector: 8 consecutive ones, chunk i TPR + tid, as one 16-byte access
-//    (every base, stride and H a multiple of 8);
-//  * kPlain: the same columns, element by element (NVFP4 output on rows that
-//    are not 16-byte aligned: a block's halves in a lane pair);
-//  * kStrided: one of every TPR columns, so that a 2-byte access of a wave
-//    covers one 128-byte run (anything else: odd H, odd strides).
-enum Access { kVector, kPlain, kStrided };
+// The columns of a row's TPR threads: thread tid holds chunks tid, TPR + tid,
+// ... of 8 columns, one 16-byte access each whatever the row's alignment.
+// When H is no multiple of 8 the last chunk is either
+//  * kOverlap (H >= 8): moved back to the row's last 8 columns, so that no
+//    access is shorter (a branch around one would make its wave wait for each
+//    operand's load in turn: one row of 1545 columns 5.2 us against 3.6 for
+//    1544).  The columns it shares with the chunk before are computed twice,
+//    to the same bits, and counted once; nothing may be stored before every
+//    thread of the row has loaded;
+//  * kShort: loaded and stored in shorter pieces.
+enum Tail { kNone, kOverlap, kShort };
 
-template <int TPR, int ACC>
+template <int TPR, int TAIL>
 struct Columns {
-  int tid;
-  int64_t H;
-  __device__ __forceinline__ int64_t col(int64_t i, int e) const {
-    return ACC == kStrided ? (i * 8 + e) * TPR + tid : (i * TPR + tid) * 8 + e;
+  int tid, H;
+  // columns of chunk i before its start is moved back, and the columns it is moved by
+  __device__ __forceinline__ int first(int i) const { return (i * TPR + tid) * 8; }
+  __device__ __forceinline__ int shared(int i) const { return TAIL == kOverlap ? max(first(i) - (H - 8), 0) : 0; }
+  __device__ __forceinline__ int col(int i) const { return first(i) - shared(i); }
+  __device__ __forceinline__ bool any(int i) const { return first(i) < H; }
+  // whether element e of chunk i counts in the row's sums
+  __device__ __forceinline__ bool counts(int i, int e) const {
+    if (TAIL == kOverlap) return any(i) && e >= shared(i);
+    return first(i) + (TAIL == kShort ? e : 0) < H;
   }
-  __device__ __forceinline__ bool valid(int64_t i, int e) const { return col(i, ACC == kVector ? 0 : e) < H; }
   // chunk i of a row or vector as packed bf16; columns past H are 0
-  __device__ __forceinline__ u4_t load(const uint16_t* row, int64_t i) const {
-    if constexpr (ACC == kVector) return valid(i, 0) ? *(const u4_t*)(row + col(i, 0)) : u4_t{0u, 0u, 0u, 0u};
-    uint32_t h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = valid(i, e) ? row[col(i, e)] : 0u;
-    return u4_t{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+  __device__ __forceinline__ u4_t load(const uint16_t* row, int i) const {
+    if (TAIL == kShort && any(i) && first(i) + 8 > H) return load_tail8(row + first(i), H & 7);
+    return any(i) ? load8(row + col(i)) : u4_t{0u, 0u, 0u, 0u};
   }
-  __device__ __forceinline__ void store(uint16_t* row, int64_t i, const float (&v)[8]) const {
-    const u4_t w = {f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]),
-                    f32x2_to_bf16x2_bits(v[4], v[5]), f32x2_to_bf16x2_bits(v[6], v[7])};
-    if constexpr (ACC == kVector) {
-      if (valid(i, 0)) *(u4_t*)(row + col(i, 0)) = w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (valid(i, e)) row[col(i, e)] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    }
+  __device__ __forceinline__ void store(uint16_t* row, int i, const float (&v)[8]) const {
+    if (TAIL == kShort && any(i) && first(i) + 8 > H) store_tail8(row + first(i), to_bf16x8(v), H & 7);
+    else if (any(i)) store8(row + col(i), to_bf16x8(v));
   }
 };
-
-__device__ __forceinline__ float bf16_at(u4_t w, int e) {
-  return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-}
 
 template <int CTRL>
 __device__ __forceinline__ double dpp_add(double v) {
@@ -73,6 +66,25 @@ __device__ __forceinline__ double dpp_add(double v) {
   const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, false);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
   return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// v + its value in the neighbouring group of 16 or 32 lanes: a swap of a value
+// with itself leaves both groups' values in every lane.
+__device__ __forceinline__ double join(u2_t lo, u2_t hi) {
+  return __builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]) +
+         __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]);
+}
+__device__ __forceinline__ double add_swap16(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+  return join(__builtin_bit_cast(u2_t, __builtin_amdgcn_permlane16_swap(lo, lo, false, false)),
+              __builtin_bit_cast(u2_t, __builtin_amdgcn_permlane16_swap(hi, hi, false, false)));
+}
+__device__ __forceinline__ double add_swap32(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+  return join(__builtin_bit_cast(u2_t, __builtin_amdgcn_permlane32_swap(lo, lo, false, false)),
+              __builtin_bit_cast(u2_t, __builtin_amdgcn_permlane32_swap(hi, hi, false, false)));
 }
 
 // Sum over the TPR threads of a row, in a fixed order, to all of them.  Every
@@ -83,8 +95,8 @@ __device__ __forceinline__ double row_sum(double v, double* cell) {
   v = dpp_add<0x4E>(v);   // lane ^ 2
   v = dpp_add<0x141>(v);  // mirror of 8 lanes
   v = dpp_add<0x140>(v);  // mirror of 16 lanes
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
+  v = add_swap16(v);
+  v = add_swap32(v);
   if constexpr (TPR > 64) {
     __syncthreads();  // the cells' last readers are done
     if ((threadIdx.x & 63) == 0) cell[threadIdx.x >> 6] = v;
@@ -102,8 +114,16 @@ struct Stats {
   float rstd;
 };
 
-__device__ __forceinline__ float rstd_of(double sq, int64_t H, float eps) {
-  return (float)(1.0 / sqrt(sq / (double)H + (double)eps));
+// 1 / sqrt(ms + eps), in fp64 rounded once to fp32: the hardware estimate and
+// two Newton steps (each at least doubles its 23 bits), a quarter of the
+// latency of a square root and a division.  An infinite sum gives 0.
+__device__ __forceinline__ float rstd_of(double ms, float eps) {
+  const double v = ms + (double)eps;
+  const double y0 = __builtin_amdgcn_rsq(v);
+  const double h = 0.5 * v;
+  double y = y0 * __builtin_fma(-h * y0, y0, 1.5);
+  y = y * __builtin_fma(-h * y, y, 1.5);
+  return (float)(v < 1e300 && v > 1e-300 ? y : y0);
 }
 
 __device__ __forceinline__ float normed(float v, const Stats& s, bool layer, float w, bool has_w, float b, bool has_b) {
@@ -113,9 +133,9 @@ __device__ __forceinline__ float normed(float v, const Stats& s, bool layer, flo
   return y;
 }
 
-// Statistics of a row held as V chunks of 8 per thread (columns past H are 0).
-template <int TPR, int V, int ACC>
-__device__ __forceinline__ Stats row_stats(const float (&v)[V][8], const Columns<TPR, ACC>& at, const NormLaunch& p,
+// Statistics of a row held as V chunks of 8 per thread.
+template <int TPR, int V, int TAIL>
+__device__ __forceinline__ Stats row_stats(const float (&v)[V][8], const Columns<TPR, TAIL>& at, const NormLaunch& p,
                                            double* cell) {
   Stats s{0.0, 0.0f};
   if (p.layer) {
@@ -123,29 +143,29 @@ __device__ __forceinline__ Stats row_stats(const float (&v)[V][8], const Columns
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a += (double)v[i][e];
-    s.mean = row_sum<TPR>(a, cell) / (double)p.H;
+      for (int e = 0; e < 8; ++e) a += at.counts(i, e) ? (double)v[i][e] : 0.0;
+    s.mean = row_sum<TPR>(a, cell) * p.inv_h;
   }
   double q = 0.0;
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const double d = (double)v[i][e] - s.mean;
-      if (at.valid(i, e)) q = __builtin_fma(d, d, q);
+      const double d = at.counts(i, e) ? (double)v[i][e] - s.mean : 0.0;
+      q = __builtin_fma(d, d, q);
     }
-  s.rstd = rstd_of(row_sum<TPR>(q, cell), p.H, p.eps);
+  s.rstd = rstd_of(row_sum<TPR>(q, cell) * p.inv_h, p.eps);
   return s;
 }
 
 // y of one chunk, to bf16 and NVFP4
-template <int TPR, int ACC>
-__device__ __forceinline__ void store_y(const NormLaunch& p, const Columns<TPR, ACC>& at, int64_t t, int64_t i,
+template <int TPR, int TAIL>
+__device__ __forceinline__ void store_y(const NormLaunch& p, const Columns<TPR, TAIL>& at, int64_t t, int i,
                                         const float (&y)[8], float gs) {
   if (p.y) at.store(p.y + t * p.ldy, i, y);
-  if constexpr (ACC != kStrided) {
-    const int64_t c = at.col(i, 0);
-    if (p.q && c < p.H) {
+  if constexpr (TAIL == kNone) {
+    const int c = at.col(i);
+    if (p.q && c < at.H) {
       // H % 16 == 0: the lanes of a pair hold the two halves of a block
       uint32_t codes;
       const uint32_t sf = quantize_half_block16(f4_t{y[0], y[1], y[2], y[3]}, f4_t{y[4], y[5], y[6], y[7]}, gs, codes);
@@ -163,12 +183,12 @@ __device__ __forceinline__ void store_y(const NormLaunch& p, const Columns<TPR, 
 template <int TPR>
 constexpr int kRowsPerGroup = TPR == 64 ? 4 : 1;  // rows of one work-group
 
-template <int TPR, int V, int ACC>
+template <int TPR, int V, int TAIL>
 __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(NormLaunch p) {
   __shared__ double cell[TPR / 64];
   const int64_t t = (int64_t)blockIdx.x * kRowsPerGroup<TPR> + threadIdx.x / TPR;
   if (t >= p.T) return;  // whole waves: a row has 64 threads, or the work-group
-  const Columns<TPR, ACC> at{(int)threadIdx.x % TPR, p.H};
+  const Columns<TPR, TAIL> at{(int)threadIdx.x % TPR, (int)p.H};
   const uint16_t* gate = p.gate ? p.gate + (p.gate_group > 0 ? t / p.gate_group : 0) * p.H : nullptr;
   u4_t x[V], res[V];
 #pragma unroll
@@ -182,7 +202,7 @@ __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(Norm
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[i][e] = bf16_at(x[i], e);
   Stats s{0.0, 0.0f};
-  if (p.post_w) s = row_stats<TPR, V, ACC>(v, at, p, cell);
+  if (p.post_w) s = row_stats<TPR, V, TAIL>(v, at, p, cell);
   u4_t pw[V], pb[V], g[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -198,12 +218,17 @@ __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(Norm
         v[i][e] = normed(v[i][e], s, p.layer, bf16_at(pw[i], e), true, p.post_b ? bf16_at(pb[i], e) : 0.0f, p.post_b);
       if (gate) v[i][e] = bf16_at(g[i], e) * v[i][e];
       if (p.res) v[i][e] = p.beta * bf16_at(res[i], e) + v[i][e];
-      if (!at.valid(i, e)) v[i][e] = 0.0f;  // stays out of the sums
     }
-    if (p.r) at.store(p.r + t * p.ldr, i, v[i]);
+    if (TAIL == kNone && p.r) at.store(p.r + t * p.ldr, i, v[i]);
   }
-  if (!p.y && !p.q) return;
-  s = row_stats<TPR, V, ACC>(v, at, p, cell);
+  const bool norm = p.y || p.q;
+  if (TAIL == kOverlap && TPR > 64) __syncthreads();  // the whole row is loaded: r may be x or res
+  if (TAIL != kNone && p.r) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) at.store(p.r + t * p.ldr, i, v[i]);
+  }
+  if (!norm) return;
+  s = row_stats<TPR, V, TAIL>(v, at, p, cell);
   u4_t w[V], b[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -220,24 +245,24 @@ __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(Norm
   }
 }
 
-// Rows too long for the registers: the same steps with the row read again for
+// Rows too long for the registers (and those below 8 columns): the same steps with the row read again for
 // each sum, one work-group per row.  A thread stores only columns it reads,
 // after its last read of them, so r may be x or res here too.
-template <int ACC>
+template <int TAIL>
 __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
   constexpr int TPR = 1024;
   __shared__ double cell[TPR / 64];
   const int64_t t = blockIdx.x, H = p.H;
-  const Columns<TPR, ACC> at{(int)threadIdx.x, H};
+  const Columns<TPR, TAIL> at{(int)threadIdx.x, (int)H};
   const uint16_t* gate = p.gate ? p.gate + (p.gate_group > 0 ? t / p.gate_group : 0) * H : nullptr;
-  const int64_t n = (H + 8 * TPR - 1) / (8 * TPR);
+  const int n = (int)((H + 8 * TPR - 1) / (8 * TPR));
   Stats sx{0.0, 0.0f}, sr{0.0, 0.0f};
-  auto x_chunk = [&](int64_t i, float (&v)[8]) {
+  auto x_chunk = [&](int i, float (&v)[8]) {
     const u4_t x = at.load(p.x + t * p.ldx, i);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = bf16_at(x, e);
   };
-  auto r_chunk = [&](int64_t i, float (&v)[8]) {
+  auto r_chunk = [&](int i, float (&v)[8]) {
     const u4_t none = {0u, 0u, 0u, 0u};
     const u4_t res = p.res ? at.load(p.res + t * p.ldres, i) : none;
     const u4_t pw = p.post_w ? at.load(p.post_w, i) : none, pb = p.post_b ? at.load(p.post_b, i) : none;
@@ -255,31 +280,31 @@ __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
     float v[8];
     if (p.layer) {
       double a = 0.0;
-      for (int64_t i = 0; i < n; ++i) {
+      for (int i = 0; i < n; ++i) {
         chunk(i, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (at.valid(i, e)) a += (double)v[e];
+          if (at.counts(i, e)) a += (double)v[e];
       }
-      s.mean = row_sum<TPR>(a, cell) / (double)H;
+      s.mean = row_sum<TPR>(a, cell) * p.inv_h;
     }
     double q = 0.0;
-    for (int64_t i = 0; i < n; ++i) {
+    for (int i = 0; i < n; ++i) {
       chunk(i, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const double d = (double)v[e] - s.mean;
-        if (at.valid(i, e)) q = __builtin_fma(d, d, q);
+        if (at.counts(i, e)) q = __builtin_fma(d, d, q);
       }
     }
-    s.rstd = rstd_of(row_sum<TPR>(q, cell), H, p.eps);
+    s.rstd = rstd_of(row_sum<TPR>(q, cell) * p.inv_h, p.eps);
     return s;
   };
   const bool norm = p.y || p.q;
   if (p.post_w) sx = stats(x_chunk);
   if (norm) sr = stats(r_chunk);
   const float gs = p.q && p.gs ? *p.gs : 1.0f;
-  for (int64_t i = 0; i < n; ++i) {
+  for (int i = 0; i < n; ++i) {
     float v[8];
     r_chunk(i, v);
     if (p.r) at.store(p.r + t * p.ldr, i, v);
@@ -296,16 +321,14 @@ template <int TPR, int V>
 static void launch_norm(const NormLaunch& p, hipStream_t stream) {
   constexpr int R = kRowsPerGroup<TPR>;
   const dim3 grid((unsigned)((p.T + R - 1) / R)), block(TPR * R);
-  if (p.vec) hipLaunchKernelGGL((k_residual_norm<TPR, V, kVector>), grid, block, 0, stream, p);
-  else if (p.q) hipLaunchKernelGGL((k_residual_norm<TPR, V, kPlain>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((k_residual_norm<TPR, V, kStrided>), grid, block, 0, stream, p);
+  if (p.H % 8 == 0) hipLaunchKernelGGL((k_residual_norm<TPR, V, kNone>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((k_residual_norm<TPR, V, kOverlap>), grid, block, 0, stream, p);
 }
 
 static void launch_norm_long(const NormLaunch& p, hipStream_t stream) {
   const dim3 grid((unsigned)p.T), block(1024);
-  if (p.vec) hipLaunchKernelGGL((k_residual_norm_long<kVector>), grid, block, 0, stream, p);
-  else if (p.q) hipLaunchKernelGGL((k_residual_norm_long<kPlain>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((k_residual_norm_long<kStrided>), grid, block, 0, stream, p);
+  if (p.H % 8 == 0) hipLaunchKernelGGL((k_residual_norm_long<kNone>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((k_residual_norm_long<kShort>), grid, block, 0, stream, p);
 }
 
 // Threads per row and chunks per thread.  Up to two rows per CU a call is one
@@ -317,7 +340,7 @@ static void launch_norm_long(const NormLaunch& p, hipStream_t stream) {
 // 512 x 3 117, 1024 x 2 135; a wave a row, 64 x 12, holds too few waves: 354).
 hipError_t launch_residual_norm(const NormLaunch& p, hipStream_t stream) {
   const int64_t n8 = (p.H + 7) / 8;
-  if (n8 > 2048) launch_norm_long(p, stream);
+  if (n8 > 2048 || p.H < 8) launch_norm_long(p, stream);
   else if (n8 > 1536) launch_norm<1024, 2>(p, stream);
   else if (n8 <= 64) launch_norm<64, 1>(p, stream);
   else if (p.T <= 2 * kCUs) {

@@ -108,7 +108,7 @@ def test_norm_refusals():
     for name in ("x", "post_w", "gate", "res", "w", "b", "r", "y"):
         assert _norm(**{name: FAKE + 1}) == ALIGN
     assert _norm(gs=FAKE + 2, q=FAKE, sf=FAKE) == ALIGN
-    assert _norm(T=1 << 31) == UNSUPPORTED
+    assert _norm(T=1 << 31) == UNSUPPORTED and _norm(H=(1 << 30) + 1) == UNSUPPORTED
     assert _norm(T=0, x=None, y=None) == 0
 
 

@@ -101,6 +101,20 @@ def test_row_strides_offsets_and_padding(M, N, ldr, ldd, off):
     assert (whole[mask] == -5.0).all(), "padding of d was written"
 
 
+@pytest.mark.parametrize("M", [5, 300])
+def test_rows_past_32_bit_offsets(M):
+    # the last row of d and residual starts past 2^33 bytes (register and LDS tiles)
+    N, K, alpha = 40, 512, np.float32(ALPHA)
+    ld = -(-(1 << 32) // (M - 1)) + 8
+    ops, xa, xb, bv, rv = _case(M, N, K, 950, True, True)
+    big = torch.empty((M - 1) * ld + 2 * N, dtype=torch.bfloat16, device="cuda")
+    r, d = big.as_strided((M, N), (ld, 1), 0), big.as_strided((M, N), (ld, 1), N)
+    r.copy_(dev_bf16(rv))
+    nv.nvfp4_gemm_epilogue(*ops, scalar(alpha), dev_bf16(bv), 0, r, 1.0, d, M, N, K, nv.gemm_epilogue_workspace(M, N, K))
+    y, err = br.epilogue(xa, xb, alpha, bv, 0, rv, 1.0)
+    close(values(d), y, br.bf16_bound(y, err), "far rows")
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 768, 512), (64, 768, 6144), (1024, 256, 6144), (700, 1000, 512)])
 def test_residual_in_place(M, N, K):
     ops, xa, xb, _, rv = _case(M, N, K, 40 + M, False, True)

@@ -158,6 +158,20 @@ def test_row_strides_offsets_and_padding(H, ld, off):
         assert (host(f.float())[mask] == -5.0).all(), "padding was written"
 
 
+def test_rows_past_32_bit_offsets():
+    # rows 2^30 + 8 elements apart: the last starts past 2^33 bytes
+    T, H, ld = 5, 272, (1 << 30) + 8
+    c = _case(T, H, 12, nv.NORM_RMS, True, None, True)
+    r32, y32 = br.residual_norm(**c)
+    big = torch.empty(4 * ld + 4 * H, dtype=torch.bfloat16, device="cuda")
+    x, res, r, y = [big.as_strided((T, H), (ld, 1), i * H) for i in range(4)]
+    x.copy_(dev_bf16(c["x"]))
+    res.copy_(dev_bf16(c["res"]))
+    _run(c, T, H, r, y, x=x, res=res)
+    _same_bits(r.contiguous(), r32, "r")
+    _same_bits(y.contiguous(), y32, "y")
+
+
 @pytest.mark.parametrize("kind", [nv.NORM_RMS, nv.NORM_LAYER])
 def test_zero_constant_and_large_rows(kind):
     # a zero row gives zeros (rstd = 1 / sqrt(eps)); a constant row has no variance; large values neither
