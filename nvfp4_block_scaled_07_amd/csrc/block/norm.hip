@@ -126,19 +126,26 @@ __device__ __forceinline__ float rstd_of(double ms, float eps) {
   return (float)(v < 1e300 && v > 1e-300 ? y : y0);
 }
 
-__device__ __forceinline__ float normed(float v, const Stats& s, bool layer, float w, bool has_w, float b, bool has_b) {
-  float y = (layer ? (float)((double)v - s.mean) : v) * s.rstd;
-  if (has_w) y = y * w;
-  if (has_b) y = y + b;
-  return y;
+// Absent vectors stand for values that change no bit: weights and gates of 1,
+// biases of -0.
+constexpr uint32_t kOnes = 0x3F803F80u, kMinusZeros = 0x80008000u;
+
+template <bool LAYER>
+__device__ __forceinline__ float normed(float v, const Stats& s, float w, float b) {
+  return (LAYER ? (float)((double)v - s.mean) : v) * s.rstd * w + b;
+}
+
+template <class C>
+__device__ __forceinline__ u4_t load_or(const C& at, const uint16_t* row, int i, uint32_t absent) {
+  return row ? at.load(row, i) : u4_t{absent, absent, absent, absent};
 }
 
 // Statistics of a row held as V chunks of 8 per thread.
-template <int TPR, int V, int TAIL>
+template <int TPR, int V, int TAIL, bool LAYER>
 __device__ __forceinline__ Stats row_stats(const float (&v)[V][8], const Columns<TPR, TAIL>& at, const NormLaunch& p,
                                            double* cell) {
   Stats s{0.0, 0.0f};
-  if (p.layer) {
+  if constexpr (LAYER) {
     double a = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -151,7 +158,7 @@ __device__ __forceinline__ Stats row_stats(const float (&v)[V][8], const Columns
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const double d = at.counts(i, e) ? (double)v[i][e] - s.mean : 0.0;
+      const double d = at.counts(i, e) ? (LAYER ? (double)v[i][e] - s.mean : (double)v[i][e]) : 0.0;
       q = __builtin_fma(d, d, q);
     }
   s.rstd = rstd_of(row_sum<TPR>(q, cell) * p.inv_h, p.eps);
@@ -183,7 +190,7 @@ __device__ __forceinline__ void store_y(const NormLaunch& p, const Columns<TPR, 
 template <int TPR>
 constexpr int kRowsPerGroup = TPR == 64 ? 4 : 1;  // rows of one work-group
 
-template <int TPR, int V, int TAIL>
+template <int TPR, int V, int TAIL, bool LAYER>
 __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(NormLaunch p) {
   __shared__ double cell[TPR / 64];
   const int64_t t = (int64_t)blockIdx.x * kRowsPerGroup<TPR> + threadIdx.x / TPR;
@@ -201,46 +208,43 @@ __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(Norm
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[i][e] = bf16_at(x[i], e);
-  Stats s{0.0, 0.0f};
-  if (p.post_w) s = row_stats<TPR, V, TAIL>(v, at, p, cell);
-  u4_t pw[V], pb[V], g[V];
+  if (p.post_w) {
+    const Stats s = row_stats<TPR, V, TAIL, LAYER>(v, at, p, cell);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (p.post_w) pw[i] = at.load(p.post_w, i);
-    if (p.post_b) pb[i] = at.load(p.post_b, i);
-    if (gate) g[i] = at.load(gate, i);
-  }
+    for (int i = 0; i < V; ++i) {
+      const u4_t w = at.load(p.post_w, i), b = load_or(at, p.post_b, i, kMinusZeros);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (p.post_w)
-        v[i][e] = normed(v[i][e], s, p.layer, bf16_at(pw[i], e), true, p.post_b ? bf16_at(pb[i], e) : 0.0f, p.post_b);
-      if (gate) v[i][e] = bf16_at(g[i], e) * v[i][e];
-      if (p.res) v[i][e] = p.beta * bf16_at(res[i], e) + v[i][e];
+      for (int e = 0; e < 8; ++e) v[i][e] = normed<LAYER>(v[i][e], s, bf16_at(w, e), bf16_at(b, e));
     }
-    if (TAIL == kNone && p.r) at.store(p.r + t * p.ldr, i, v[i]);
+  }
+  if (gate) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const u4_t g = at.load(gate, i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = bf16_at(g, e) * v[i][e];
+    }
+  }
+  if (p.res) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = p.beta * bf16_at(res[i], e) + v[i][e];
   }
   const bool norm = p.y || p.q;
   if (TAIL == kOverlap && TPR > 64) __syncthreads();  // the whole row is loaded: r may be x or res
-  if (TAIL != kNone && p.r) {
+  if (p.r) {
 #pragma unroll
     for (int i = 0; i < V; ++i) at.store(p.r + t * p.ldr, i, v[i]);
   }
   if (!norm) return;
-  s = row_stats<TPR, V, TAIL>(v, at, p, cell);
-  u4_t w[V], b[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (p.w) w[i] = at.load(p.w, i);
-    if (p.b) b[i] = at.load(p.b, i);
-  }
+  const Stats s = row_stats<TPR, V, TAIL, LAYER>(v, at, p, cell);
   const float gs = p.q && p.gs ? *p.gs : 1.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
+    const u4_t w = load_or(at, p.w, i, kOnes), b = load_or(at, p.b, i, kMinusZeros);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[i][e] = normed(v[i][e], s, p.layer, p.w ? bf16_at(w[i], e) : 1.0f, p.w, p.b ? bf16_at(b[i], e) : 0.0f, p.b);
+    for (int e = 0; e < 8; ++e) v[i][e] = normed<LAYER>(v[i][e], s, bf16_at(w, e), bf16_at(b, e));
     store_y(p, at, t, i, v[i], gs);
   }
 }
@@ -248,7 +252,7 @@ __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(Norm
 // Rows too long for the registers (and those below 8 columns): the same steps with the row read again for
 // each sum, one work-group per row.  A thread stores only columns it reads,
 // after its last read of them, so r may be x or res here too.
-template <int TAIL>
+template <int TAIL, bool LAYER>
 __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
   constexpr int TPR = 1024;
   __shared__ double cell[TPR / 64];
@@ -263,22 +267,24 @@ __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
     for (int e = 0; e < 8; ++e) v[e] = bf16_at(x, e);
   };
   auto r_chunk = [&](int i, float (&v)[8]) {
-    const u4_t none = {0u, 0u, 0u, 0u};
-    const u4_t res = p.res ? at.load(p.res + t * p.ldres, i) : none;
-    const u4_t pw = p.post_w ? at.load(p.post_w, i) : none, pb = p.post_b ? at.load(p.post_b, i) : none;
-    const u4_t g = gate ? at.load(gate, i) : none;
+    const u4_t res = load_or(at, p.res ? p.res + t * p.ldres : nullptr, i, 0u);
     x_chunk(i, v);
+    if (p.post_w) {
+      const u4_t w = at.load(p.post_w, i), b = load_or(at, p.post_b, i, kMinusZeros);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = normed<LAYER>(v[e], sx, bf16_at(w, e), bf16_at(b, e));
+    }
+    const u4_t g = load_or(at, gate, i, kOnes);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (p.post_w) v[e] = normed(v[e], sx, p.layer, bf16_at(pw, e), true, bf16_at(pb, e), p.post_b);
-      if (gate) v[e] = bf16_at(g, e) * v[e];
+      v[e] = bf16_at(g, e) * v[e];
       if (p.res) v[e] = p.beta * bf16_at(res, e) + v[e];
     }
   };
   auto stats = [&](auto&& chunk) {
     Stats s{0.0, 0.0f};
     float v[8];
-    if (p.layer) {
+    if constexpr (LAYER) {
       double a = 0.0;
       for (int i = 0; i < n; ++i) {
         chunk(i, v);
@@ -309,26 +315,34 @@ __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
     r_chunk(i, v);
     if (p.r) at.store(p.r + t * p.ldr, i, v);
     if (!norm) continue;
-    const u4_t none = {0u, 0u, 0u, 0u};
-    const u4_t w = p.w ? at.load(p.w, i) : none, b = p.b ? at.load(p.b, i) : none;
+    const u4_t w = load_or(at, p.w, i, kOnes), b = load_or(at, p.b, i, kMinusZeros);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = normed(v[e], sr, p.layer, bf16_at(w, e), p.w, bf16_at(b, e), p.b);
+    for (int e = 0; e < 8; ++e) v[e] = normed<LAYER>(v[e], sr, bf16_at(w, e), bf16_at(b, e));
     store_y(p, at, t, i, v, gs);
   }
 }
 
-template <int TPR, int V>
-static void launch_norm(const NormLaunch& p, hipStream_t stream) {
+template <int TPR, int V, bool LAYER>
+static void launch_norm_as(const NormLaunch& p, hipStream_t stream) {
   constexpr int R = kRowsPerGroup<TPR>;
   const dim3 grid((unsigned)((p.T + R - 1) / R)), block(TPR * R);
-  if (p.H % 8 == 0) hipLaunchKernelGGL((k_residual_norm<TPR, V, kNone>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((k_residual_norm<TPR, V, kOverlap>), grid, block, 0, stream, p);
+  if (p.H % 8 == 0) hipLaunchKernelGGL((k_residual_norm<TPR, V, kNone, LAYER>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((k_residual_norm<TPR, V, kOverlap, LAYER>), grid, block, 0, stream, p);
+}
+
+template <int TPR, int V>
+static void launch_norm(const NormLaunch& p, hipStream_t stream) {
+  if (p.layer) launch_norm_as<TPR, V, true>(p, stream);
+  else launch_norm_as<TPR, V, false>(p, stream);
 }
 
 static void launch_norm_long(const NormLaunch& p, hipStream_t stream) {
   const dim3 grid((unsigned)p.T), block(1024);
-  if (p.H % 8 == 0) hipLaunchKernelGGL((k_residual_norm_long<kNone>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((k_residual_norm_long<kShort>), grid, block, 0, stream, p);
+  const bool whole = p.H % 8 == 0;
+  if (whole && p.layer) hipLaunchKernelGGL((k_residual_norm_long<kNone, true>), grid, block, 0, stream, p);
+  else if (whole) hipLaunchKernelGGL((k_residual_norm_long<kNone, false>), grid, block, 0, stream, p);
+  else if (p.layer) hipLaunchKernelGGL((k_residual_norm_long<kShort, true>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((k_residual_norm_long<kShort, false>), grid, block, 0, stream, p);
 }
 
 // Threads per row and chunks per thread.  Up to two rows per CU a call is one
