@@ -186,7 +186,9 @@ __device__ __forceinline__ void store_y(const NormLaunch& p, const Columns<TPR, 
 // the row: they come from L2, and the registers they would hold cost rows in
 // flight per CU, which are what hides the sums' barriers (16384 x 6144 with
 // both norms and a gate: 164 us against 225 with every load issued first; a
-// single row is not slower either, 3.6 us).
+// single row was not slower either).  Layer and RMS norms are kernels of their
+// own for the same reason: 84 registers instead of 130 at 256 x 3, 151 us (5.3
+// TB/s, what a copy of the same bytes takes).
 template <int TPR>
 constexpr int kRowsPerGroup = TPR == 64 ? 4 : 1;  // rows of one work-group
 
@@ -345,33 +347,25 @@ static void launch_norm_long(const NormLaunch& p, hipStream_t stream) {
   else hipLaunchKernelGGL((k_residual_norm_long<kShort, false>), grid, block, 0, stream, p);
 }
 
-// Threads per row and chunks per thread.  Up to two rows per CU a call is one
-// row's latency: a chunk a thread while a work-group can hold the row (6144
-// columns: 768 x 1 3.65 us against 4.29 for 256 x 3; 2048: 2.8 against 3.4 for
-// 128 x 2).  With more rows, few threads a row: more rows in flight per CU
-// between the barriers of the sums (16276 rows of 6144, both norms and a gate:
-// 256 x 3 162 us, 384 x 2 241, 768 x 1 224; 4096 rows of 12288: 256 x 6 100 us,
-// 512 x 3 117, 1024 x 2 135; a wave a row, 64 x 12, holds too few waves: 354).
+// Threads per row and chunks per thread.  Up to 2048 columns a chunk a thread
+// is best at every number of rows, and up to 12288 two at most.  Where rows are
+// many (more than two per CU) and both a wide and a narrow shape fit, the
+// narrow one has more rows in flight per CU between the barriers of the sums
+// (16276 rows of 6144, both norms and a gate: 256 x 3 151 us, 384 x 2 157, 768 x 1
+// 164; 6103 of 16384: 512 x 4 160, 1024 x 2 176); where they are few the wide one
+// is the shorter chain (one row of 6144: 768 x 1 2.85 us, 256 x 3 3.53).
 hipError_t launch_residual_norm(const NormLaunch& p, hipStream_t stream) {
   const int64_t n8 = (p.H + 7) / 8;
+  const bool many = p.T > 2 * kCUs;
   if (n8 > 2048 || p.H < 8) launch_norm_long(p, stream);
-  else if (n8 > 1536) launch_norm<1024, 2>(p, stream);
   else if (n8 <= 64) launch_norm<64, 1>(p, stream);
-  else if (p.T <= 2 * kCUs) {
-    if (n8 <= 128) launch_norm<128, 1>(p, stream);
-    else if (n8 <= 256) launch_norm<256, 1>(p, stream);
-    else if (n8 <= 512) launch_norm<512, 1>(p, stream);
-    else if (n8 <= 768) launch_norm<768, 1>(p, stream);
-    else if (n8 <= 1024) launch_norm<512, 2>(p, stream);
-    else launch_norm<768, 2>(p, stream);
-  } else {
-    if (n8 <= 128) launch_norm<64, 2>(p, stream);
-    else if (n8 <= 256) launch_norm<128, 2>(p, stream);
-    else if (n8 <= 512) launch_norm<256, 2>(p, stream);
-    else if (n8 <= 768) launch_norm<256, 3>(p, stream);
-    else if (n8 <= 1024) launch_norm<256, 4>(p, stream);
-    else launch_norm<256, 6>(p, stream);
-  }
+  else if (n8 <= 128) launch_norm<128, 1>(p, stream);
+  else if (n8 <= 256) launch_norm<256, 1>(p, stream);
+  else if (n8 <= 512) many ? launch_norm<256, 2>(p, stream) : launch_norm<512, 1>(p, stream);
+  else if (n8 <= 768) many ? launch_norm<256, 3>(p, stream) : launch_norm<768, 1>(p, stream);
+  else if (n8 <= 1024) launch_norm<512, 2>(p, stream);
+  else if (n8 <= 1536) launch_norm<768, 2>(p, stream);
+  else many ? launch_norm<512, 4>(p, stream) : launch_norm<1024, 2>(p, stream);
   return hipGetLastError();
 }
 
