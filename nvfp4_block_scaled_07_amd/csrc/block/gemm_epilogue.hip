@@ -31,7 +31,13 @@ typedef KCfg<32, 32, 4, 3, 2, 0, 1> GatedReg32x16;
 // loop, so that after the K-groups' sum (in wave order, and over the splits
 // in split order) only arithmetic and one store remain.  A thread owns single
 // outputs, 16 consecutive lanes 16 columns of a row: one NVFP4 block.
-template <class C, bool QUANT>
+//
+// SKIP leaves the products of K units past the end of a wave's share out
+// instead of adding zeros (one token 6144 x 2048: 5.7 us against 6.3, 61 x 777 x
+// 1280: 4.4 against 5.0); where every slot is filled its branches only cut the
+// instruction schedule (1 x 4096 x 6144: 7.5 against 7.05), so the launcher
+// picks by the shape.
+template <class C, bool QUANT, bool SKIP>
 __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::OCC))) void k_gemm_kreg_epilogue(
     EpilogueLaunch p) {
   __shared__ __attribute__((aligned(16))) float red[C::KS * C::kTileFloats];
@@ -42,8 +48,11 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
   static_assert(kCols % 16 == 0, "whole NVFP4 blocks in a row of lanes");
   const int tiles_n = (int)p.g.tiles_n, S = p.g.splits;
   const int L = xcd_remap(blockIdx.x, (int)(p.g.tiles_m * p.g.tiles_n) * S);
-  const int tile = L / S, z = L % S;
-  const int64_t m0 = (int64_t)(tile / tiles_n) * C::BM, n0 = (int64_t)(tile % tiles_n) * kCols;
+  // uniform shortcuts past the integer divisions (about 100 cycles each) for
+  // unsplit calls and for one row of tiles
+  const int tile = S == 1 ? L : L / S, z = L - tile * S;
+  const int tm = p.g.tiles_m == 1 ? 0 : tile / tiles_n;
+  const int64_t m0 = (int64_t)tm * C::BM, n0 = (int64_t)(tile - tm * tiles_n) * kCols;
   const int rows_a = (int)min<int64_t>(C::BM, p.g.M - m0), rows_b = (int)min<int64_t>(kCols, p.cols - n0);
   const float a0 = p.g.alpha ? p.g.alpha[0] : 1.0f;
   const float a1 = kGated && p.g.alpha ? p.g.alpha[1] : 1.0f;
@@ -55,7 +64,7 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
     sc[k] = load_scalars<kGated>(p, a0, a1, m0 + row, n0 + col, row < rows_a && col < rows_b);
   }
   Mfma<16>::Acc acc[C::TM][C::TN];
-  kreg_accumulate<C, 0>(p.g, m0, n0, rows_a, rows_b, z, S, acc);
+  kreg_accumulate<C, 0, SKIP>(p.g, m0, n0, rows_a, rows_b, z, S, acc);
   const int lane = threadIdx.x & 63, wave = wave_id();
   float* mine = red + wave * C::kTileFloats;
 #pragma unroll
@@ -110,7 +119,12 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
 
 template <class C, bool QUANT>
 static void launch_kreg_epilogue(const EpilogueLaunch& p, unsigned grid, hipStream_t stream) {
-  hipLaunchKernelGGL((k_gemm_kreg_epilogue<C, QUANT>), dim3(grid), dim3(C::kThreads), 0, stream, p);
+  // K units of the longest split, and whether they fill every wave's slots
+  const int64_t units = (p.g.K / C::kUnit + p.g.splits - 1) / p.g.splits;
+  if (units % (C::KS * C::D) == 0)
+    hipLaunchKernelGGL((k_gemm_kreg_epilogue<C, QUANT, false>), dim3(grid), dim3(C::kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((k_gemm_kreg_epilogue<C, QUANT, true>), dim3(grid), dim3(C::kThreads), 0, stream, p);
 }
 
 // Plan kinds that only the block GEMMs have, numbered past the plain GEMM's.
@@ -164,20 +178,24 @@ static const PlanKind kGated10 = {"gatedreg16x16", 16, 16, 256, true, true, fals
 static const PlanKind kGated12 = {"gatedreg32x16", 32, 16, 256, true, true, false, GatedReg32x16::KS, GatedReg32x16::D};
 static const PlanKind kGated32 = {"gatedreg16x32", 16, 32, 256, true, true, false, GatedReg16x32::KS, GatedReg16x32::D};
 
-// The plain GEMM's rules on the tiles of both matrices: register tiles up to
-// M = 128 while they need at most one work-group per CU, 256-row tiles once
-// they fill the CUs twice, 128-row tiles three times, else split 64-row tiles.
-// Up to M = 16 wider matrices take 16 x 32 register tiles (16 x 6144 x 2048
-// outputs: 8.6 us against 11.9 for 32 x 16; 16 x 16384 x 6144: 30.6 against 38).
+// From sweeps of M = 32..4096, I = 1024..16384, K = 2048 and 6144.  Register
+// tiles up to M = 128 while they need at most one work-group per CU; up to M =
+// 16 wider matrices take 16 x 32 register tiles (16 x 6144 x 2048 outputs: 8.6 us
+// against 11.9 for 32 x 16; 16 x 16384 x 6144: 30.6 against 38).  256-row tiles
+// (one work-group per CU) where their last round is at least 85% full in the
+// mean (2048 x 4096 x 6144, one full round: 163 us against 191 on 128-row
+// tiles; 1024 x 4096, half a round: 133 against 100), 128-row tiles from one
+// round of two work-groups per CU on (1024 x 4096 x 6144: 100 us against 108.5 on
+// 64-row tiles; half a round: 59 against 57), else split 64-row tiles.
 GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K) {
   auto tiles = [&](const PlanKind& k) { return ((M + k.bm - 1) / k.bm) * ((I + k.bn - 1) / k.bn); };
+  const int64_t t14 = tiles(kGated14), rounds14 = (t14 + kCUs - 1) / kCUs;
   int kind = 9;
   if (M <= 128 && tiles(kGated10) <= kCUs) kind = 10;
   else if (M <= 16 && tiles(kGated32) <= 4 * kCUs) kind = kReg16x32;
   else if (M <= 128 && tiles(kGated12) <= kCUs) kind = 12;
-  else if (M <= 32 && tiles(kGated12) <= 4 * kCUs) kind = 12;
-  else if (M > 64 && tiles(kGated14) >= 2 * kCUs) kind = 14;
-  else if (M > 64 && tiles(kGated15) >= 3 * kCUs) kind = 15;
+  else if (M > 64 && t14 * 100 >= rounds14 * kCUs * 85) kind = 14;
+  else if (M > 64 && tiles(kGated15) >= 2 * kCUs) kind = 15;
   int fk = -1, fs = 0;
   auto has = [](int k) { return k == 9 || k == 10 || k == 12 || k == 14 || k == 15 || k == kReg16x32; };
   if (forced_plan(kForceGemm, &fk, &fs) && has(fk)) kind = fk;

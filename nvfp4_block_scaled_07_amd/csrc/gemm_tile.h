@@ -555,29 +555,37 @@ __device__ __forceinline__ void zero_acc(typename C::Acc (&acc)[C::TM][C::TN]) {
       for (int j = 0; j < Mfma<C::MF>::kAcc; ++j) acc[tm][tn][j] = 0.0f;
 }
 
+// A main loop calls hook(left) in every stage after issuing its DMA, left
+// being the stages not yet computed (this one included): a place to start
+// loads for the epilogue under the last stages' MFMAs.
+struct NoHook {
+  __device__ __forceinline__ void operator()(int) const {}
+};
+
 // Stages i0 + J, i0 + J + 1, ... (J < STAGES) of the main loop: issue the DMA
 // of the stage STAGES - 1 ahead, compute this one, wait for the next.
-template <class C, int J>
+template <class C, int J, class F>
 __device__ __forceinline__ void stage_steps(Smem<C>& sm, const ReadAddr<C>& ra, const Operand& A, const Operand& B,
                                             int i0, int n, int kt0, int wave, int lane, int a_rows_dma,
-                                            int tm_active, typename C::Acc (&acc)[C::TM][C::TN]) {
+                                            int tm_active, typename C::Acc (&acc)[C::TM][C::TN], const F& hook) {
   if constexpr (J < C::STAGES) {
     const int i = i0 + J;
     if (i >= n) return;
     const int pre = i + C::STAGES - 1;
     if (pre < n) issue_stage<C>(sm, (J + C::STAGES - 1) % C::STAGES, A, B, kt0 + pre, wave, lane, a_rows_dma);
+    hook(n - i);
     compute_stage<C, J>(sm, ra, tm_active, acc);
     if (i + 1 < n) stage_ready<C>(min(C::STAGES - 2, n - 2 - i));
-    stage_steps<C, J + 1>(sm, ra, A, B, i0, n, kt0, wave, lane, a_rows_dma, tm_active, acc);
+    stage_steps<C, J + 1>(sm, ra, A, B, i0, n, kt0, wave, lane, a_rows_dma, tm_active, acc, hook);
   }
 }
 
 // K-tiles [kt0, kt1) of the tile into acc (which is zeroed first).  Loads run
 // STAGES - 1 stages ahead of the MFMAs; each wait only drains the stage needed
 // next, so the later stages stay in flight across the barrier.
-template <class C>
+template <class C, class F = NoHook>
 __device__ __forceinline__ void mainloop(Smem<C>& sm, const Operand& A, const Operand& B, int kt0, int kt1,
-                                         int tm_active, typename C::Acc (&acc)[C::TM][C::TN]) {
+                                         int tm_active, typename C::Acc (&acc)[C::TM][C::TN], const F& hook = F()) {
   const int tid = threadIdx.x;
   const int lane = tid & 63, wave = wave_id();
   zero_acc<C>(acc);
@@ -596,7 +604,7 @@ __device__ __forceinline__ void mainloop(Smem<C>& sm, const Operand& A, const Op
   const ReadAddr<C> ra = read_addr<C>(sm);
   // unrolled by STAGES: each stage buffer's LDS offset is a constant
   for (int i0 = 0; i0 < n; i0 += C::STAGES)
-    stage_steps<C, 0>(sm, ra, A, B, i0, n, kt0, wave, lane, a_rows_dma, tm_active, acc);
+    stage_steps<C, 0>(sm, ra, A, B, i0, n, kt0, wave, lane, a_rows_dma, tm_active, acc, hook);
 }
 
 // alpha * acc -> bf16 stores; bounds checks only for partial tiles.

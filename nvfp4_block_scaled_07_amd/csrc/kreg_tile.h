@@ -152,11 +152,66 @@ __device__ __forceinline__ void kreg_load(KRegs<C>& R, int u, int unit, bool liv
   }
 }
 
+// Multiply-accumulate slot u's unit into acc.
+template <class C>
+__device__ __forceinline__ void kreg_unit(KRegs<C>& R, int u, bool lo8, int g, Mfma<16>::Acc (&acc)[C::TM][C::TN]) {
+#pragma unroll
+  for (int tm = 0; tm < C::TM; ++tm) kreg_exchange(R.aq[u][tm], lo8);
+#pragma unroll
+  for (int tn = 0; tn < C::TN; ++tn) kreg_exchange(R.bq[u][tn], lo8);
+  if constexpr (C::kMx) {
+    typedef int v8i_t __attribute__((ext_vector_type(8)));
+    const int ssh = 16 * (g & 1);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      v8i_t bv[C::TN];
+      int sb[C::TN];
+#pragma unroll
+      for (int tn = 0; tn < C::TN; ++tn) {
+        const uint32_t* w = R.bq[u][tn] + 4 * c;
+        bv[tn] = v8i_t{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+        sb[tn] = (int)(R.bs[u][tn] >> (ssh + 8 * c));
+      }
+#pragma unroll
+      for (int tm = 0; tm < C::TM; ++tm) {
+        const uint32_t* w = R.aq[u][tm] + 4 * c;
+        const v8i_t av = v8i_t{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+        const int sa = (int)(R.as[u][tm] >> (ssh + 8 * c));
+#pragma unroll
+        for (int tn = 0; tn < C::TN; ++tn)
+          acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv[tn], acc[tm][tn], 4, 4, 0, sa, 0,
+                                                                         sb[tn]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      h2_t asp[C::TM], bsp[C::TN];
+#pragma unroll
+      for (int tm = 0; tm < C::TM; ++tm) asp[tm] = e4m3x2_to_h2(R.as[u][tm] >> (16 * c));
+#pragma unroll
+      for (int tn = 0; tn < C::TN; ++tn) bsp[tn] = e4m3x2_to_h2(R.bs[u][tn] >> (16 * c));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        h8_t bf[C::TN];
+#pragma unroll
+        for (int tn = 0; tn < C::TN; ++tn) bf[tn] = dequant8(R.bq[u][tn][4 * c + t], scale_pair(bsp[tn], t >> 1));
+#pragma unroll
+        for (int tm = 0; tm < C::TM; ++tm) {
+          const h8_t af = dequant8(R.aq[u][tm][4 * c + t], scale_pair(asp[tm], t >> 1));
+#pragma unroll
+          for (int tn = 0; tn < C::TN; ++tn) acc[tm][tn] = Mfma<16>::run(af, bf[tn], acc[tm][tn]);
+        }
+      }
+    }
+  }
+}
+
 // Split z of S (all of K when S is 1) of the BM x BN tile at row m0 of A and row n0
 // of B into this wave's accumulators (its K-group's share; the caller sums
 // the KS waves).  rows_a, rows_b: valid rows of each operand in the tile
 // (of each matrix in a gated tile); rows past them read as zero.
-template <class C, int SFL>
+template <class C, int SFL, bool SKIP = false>
 __device__ __forceinline__ void kreg_accumulate(const GemmLaunch& p, int64_t m0, int64_t n0, int rows_a, int rows_b,
                                                 int z, int S, Mfma<16>::Acc (&acc)[C::TM][C::TN]) {
   const int64_t ld = p.K / 2, lds = p.K / C::SBLK;
@@ -219,56 +274,8 @@ __device__ __forceinline__ void kreg_accumulate(const GemmLaunch& p, int64_t m0,
   for (int i0 = 0; i0 < iters; i0 += C::D) {
 #pragma unroll
     for (int u = 0; u < C::D; ++u) {
-#pragma unroll
-      for (int tm = 0; tm < C::TM; ++tm) kreg_exchange(R.aq[u][tm], lo8);
-#pragma unroll
-      for (int tn = 0; tn < C::TN; ++tn) kreg_exchange(R.bq[u][tn], lo8);
-      if constexpr (C::kMx) {
-        typedef int v8i_t __attribute__((ext_vector_type(8)));
-        const int ssh = 16 * (g & 1);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          v8i_t bv[C::TN];
-          int sb[C::TN];
-#pragma unroll
-          for (int tn = 0; tn < C::TN; ++tn) {
-            const uint32_t* w = R.bq[u][tn] + 4 * c;
-            bv[tn] = v8i_t{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-            sb[tn] = (int)(R.bs[u][tn] >> (ssh + 8 * c));
-          }
-#pragma unroll
-          for (int tm = 0; tm < C::TM; ++tm) {
-            const uint32_t* w = R.aq[u][tm] + 4 * c;
-            const v8i_t av = v8i_t{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-            const int sa = (int)(R.as[u][tm] >> (ssh + 8 * c));
-#pragma unroll
-            for (int tn = 0; tn < C::TN; ++tn)
-              acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv[tn], acc[tm][tn], 4, 4, 0, sa, 0,
-                                                                             sb[tn]);
-          }
-        }
-      } else {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        h2_t asp[C::TM], bsp[C::TN];
-#pragma unroll
-        for (int tm = 0; tm < C::TM; ++tm) asp[tm] = e4m3x2_to_h2(R.as[u][tm] >> (16 * c));
-#pragma unroll
-        for (int tn = 0; tn < C::TN; ++tn) bsp[tn] = e4m3x2_to_h2(R.bs[u][tn] >> (16 * c));
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          h8_t bf[C::TN];
-#pragma unroll
-          for (int tn = 0; tn < C::TN; ++tn) bf[tn] = dequant8(R.bq[u][tn][4 * c + t], scale_pair(bsp[tn], t >> 1));
-#pragma unroll
-          for (int tm = 0; tm < C::TM; ++tm) {
-            const h8_t af = dequant8(R.aq[u][tm][4 * c + t], scale_pair(asp[tm], t >> 1));
-#pragma unroll
-            for (int tn = 0; tn < C::TN; ++tn) acc[tm][tn] = Mfma<16>::run(af, bf[tn], acc[tm][tn]);
-          }
-        }
-      }
-      }
+      // SKIP: a unit past the end of the range adds zeros; leave them out
+      if (!SKIP || wave + (i0 + u) * C::KS < nu) kreg_unit<C>(R, u, lo8, g, acc);
       // the slot's reload stays after its last reads (old and new contents
       // share registers; no copies that would wait on the load)
       __builtin_amdgcn_sched_barrier(0);

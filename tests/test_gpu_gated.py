@@ -70,7 +70,7 @@ def test_every_plan_forced(kind, splits, M, I, K, force_plan):
     _check(M, I, K, 17 * kind + splits + M, bias=True, label=f"kind {kind}/{splits}")
 
 
-@pytest.mark.parametrize("M,I,K", [(4096, 2064, 256), (2048, 4096, 512)])
+@pytest.mark.parametrize("M,I,K", [(4096, 2064, 256), (2048, 4096, 512), (1000, 4100, 512), (130, 16400, 256)])
 def test_large_tiles(M, I, K):
     _check(M, I, K, M + I, bias=True)
 
