@@ -93,17 +93,37 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
     if (!last_flag) return;
     if (threadIdx.x == 0) reset_counter(counter);
   }
+  // Over the splits, in split order; this split's own partial comes from LDS,
+  // and the others' loads go out four at a time (one after the other they cost
+  // a round trip each, 0.4 us; past the last split they read as zero).
   auto total = [&](int row, int col) {
-    if (S == 1) return group_sum(row, col);
+    const float own = group_sum(row, col);
+    if (S == 1) return own;
     float sum = 0.f;
-    for (int zz = 0; zz < S; ++zz) sum += load_coherent(part, (uint32_t)(zz * C::kTileFloats + row * C::BN + col) * 4);
+    for (int z0 = 0; z0 < S; z0 += 4) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = load_coherent(part, (uint32_t)((z0 + i) * C::kTileFloats + row * C::BN + col) * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += z0 + i == z ? own : v[i];
+    }
     return sum;
   };
+  // all of a thread's sums before the first use
+  float s0[kPer], s1[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int x = threadIdx.x + k * C::kThreads, row = x / kCols, col = x % kCols;
+    if (x >= kOut) break;
+    s0[k] = total(row, col);
+    s1[k] = kGated ? total(row, kCols + col) : 0.0f;
+  }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int x = threadIdx.x + k * C::kThreads, row = x / kCols, col = x % kCols;
     if (x >= kOut) break;  // whole waves
-    const float v = finish_one<kGated>(p, sc[k], total(row, col), kGated ? total(row, kCols + col) : 0.0f);
+    const float v = finish_one<kGated>(p, sc[k], s0[k], s1[k]);
     const bool valid = row < rows_a && col < rows_b;
     if constexpr (QUANT) {
       uint32_t codes;
