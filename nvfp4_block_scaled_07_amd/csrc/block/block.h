@@ -49,13 +49,13 @@ struct NormLaunch {
   const float* gs;
   uint8_t* q;
   uint8_t* sf;
-  int64_t T, H;
+  int64_t t0, T, H;              // rows t0 .. T - 1 of a launch
   int64_t ldx, ldres, ldr, ldy;  // row strides in elements
   int64_t gate_group;            // rows that share a gate row; 0: all of them
   float beta, eps;
   double inv_h;                  // 1 / H
   int layer;                     // 0: RMS, 1: mean removed first
 };
-hipError_t launch_residual_norm(const NormLaunch& p, hipStream_t stream);
+hipError_t launch_residual_norm(NormLaunch p, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -195,7 +195,7 @@ constexpr int kRowsPerGroup = TPR == 64 ? 4 : 1;  // rows of one work-group
 template <int TPR, int V, int TAIL, bool LAYER>
 __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(NormLaunch p) {
   __shared__ double cell[TPR / 64];
-  const int64_t t = (int64_t)blockIdx.x * kRowsPerGroup<TPR> + threadIdx.x / TPR;
+  const int64_t t = p.t0 + (int64_t)blockIdx.x * kRowsPerGroup<TPR> + threadIdx.x / TPR;
   if (t >= p.T) return;  // whole waves: a row has 64 threads, or the work-group
   const Columns<TPR, TAIL> at{(int)threadIdx.x % TPR, (int)p.H};
   const uint16_t* gate = p.gate ? p.gate + (p.gate_group > 0 ? t / p.gate_group : 0) * p.H : nullptr;
@@ -251,14 +251,14 @@ __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(Norm
   }
 }
 
-// Rows too long for the registers (and those below 8 columns): the same steps with the row read again for
+// Rows too long for the registers: the same steps with the row read again for
 // each sum, one work-group per row.  A thread stores only columns it reads,
 // after its last read of them, so r may be x or res here too.
 template <int TAIL, bool LAYER>
 __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
   constexpr int TPR = 1024;
   __shared__ double cell[TPR / 64];
-  const int64_t t = blockIdx.x, H = p.H;
+  const int64_t t = p.t0 + blockIdx.x, H = p.H;
   const Columns<TPR, TAIL> at{(int)threadIdx.x, (int)H};
   const uint16_t* gate = p.gate ? p.gate + (p.gate_group > 0 ? t / p.gate_group : 0) * H : nullptr;
   const int n = (int)((H + 8 * TPR - 1) / (8 * TPR));
@@ -324,10 +324,14 @@ __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
   }
 }
 
+// Rows of one launch: a launch has fewer than 2^32 threads.
+static constexpr int64_t kLaunchRows = int64_t(1) << 21;
+static int64_t launch_rows(const NormLaunch& p) { return p.T - p.t0 < kLaunchRows ? p.T - p.t0 : kLaunchRows; }
+
 template <int TPR, int V, bool LAYER>
 static void launch_norm_as(const NormLaunch& p, hipStream_t stream) {
   constexpr int R = kRowsPerGroup<TPR>;
-  const dim3 grid((unsigned)((p.T + R - 1) / R)), block(TPR * R);
+  const dim3 grid((unsigned)((launch_rows(p) + R - 1) / R)), block(TPR * R);
   if (p.H % 8 == 0) hipLaunchKernelGGL((k_residual_norm<TPR, V, kNone, LAYER>), grid, block, 0, stream, p);
   else hipLaunchKernelGGL((k_residual_norm<TPR, V, kOverlap, LAYER>), grid, block, 0, stream, p);
 }
@@ -338,8 +342,14 @@ static void launch_norm(const NormLaunch& p, hipStream_t stream) {
   else launch_norm_as<TPR, V, false>(p, stream);
 }
 
+static void launch_norm_short(const NormLaunch& p, hipStream_t stream) {
+  const dim3 grid((unsigned)((launch_rows(p) + 3) / 4)), block(256);
+  if (p.layer) hipLaunchKernelGGL((k_residual_norm<64, 1, kShort, true>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((k_residual_norm<64, 1, kShort, false>), grid, block, 0, stream, p);
+}
+
 static void launch_norm_long(const NormLaunch& p, hipStream_t stream) {
-  const dim3 grid((unsigned)p.T), block(1024);
+  const dim3 grid((unsigned)launch_rows(p)), block(1024);
   const bool whole = p.H % 8 == 0;
   if (whole && p.layer) hipLaunchKernelGGL((k_residual_norm_long<kNone, true>), grid, block, 0, stream, p);
   else if (whole) hipLaunchKernelGGL((k_residual_norm_long<kNone, false>), grid, block, 0, stream, p);
@@ -354,10 +364,11 @@ static void launch_norm_long(const NormLaunch& p, hipStream_t stream) {
 // (16276 rows of 6144, both norms and a gate: 256 x 3 151 us, 384 x 2 157, 768 x 1
 // 164; 6103 of 16384: 512 x 4 160, 1024 x 2 176); where they are few the wide one
 // is the shorter chain (one row of 6144: 768 x 1 2.85 us, 256 x 3 3.53).
-hipError_t launch_residual_norm(const NormLaunch& p, hipStream_t stream) {
+static void launch_norm_rows(const NormLaunch& p, hipStream_t stream) {
   const int64_t n8 = (p.H + 7) / 8;
   const bool many = p.T > 2 * kCUs;
-  if (n8 > 2048 || p.H < 8) launch_norm_long(p, stream);
+  if (n8 > 2048) launch_norm_long(p, stream);
+  else if (p.H < 8) launch_norm_short(p, stream);
   else if (n8 <= 64) launch_norm<64, 1>(p, stream);
   else if (n8 <= 128) launch_norm<128, 1>(p, stream);
   else if (n8 <= 256) launch_norm<256, 1>(p, stream);
@@ -366,6 +377,10 @@ hipError_t launch_residual_norm(const NormLaunch& p, hipStream_t stream) {
   else if (n8 <= 1024) launch_norm<512, 2>(p, stream);
   else if (n8 <= 1536) launch_norm<768, 2>(p, stream);
   else many ? launch_norm<512, 4>(p, stream) : launch_norm<1024, 2>(p, stream);
+}
+
+hipError_t launch_residual_norm(NormLaunch p, hipStream_t stream) {
+  for (p.t0 = 0; p.t0 < p.T; p.t0 += kLaunchRows) launch_norm_rows(p, stream);
   return hipGetLastError();
 }
 

@@ -158,6 +158,29 @@ def test_row_strides_offsets_and_padding(H, ld, off):
         assert (host(f.float())[mask] == -5.0).all(), "padding was written"
 
 
+@pytest.mark.parametrize("T,H", [((1 << 21) + 5, 4), ((1 << 21) + 3, 24)])
+def test_more_rows_than_one_launch(T, H):
+    # rows repeat with period 1001, so that a few of them stand for all
+    c = _case(1001, H, 14, nv.NORM_LAYER, True, None, True)
+    r32, y32 = br.residual_norm(**c)
+    rows = torch.arange(T, device="cuda") % 1001
+    x, res = dev_bf16(c["x"])[rows], dev_bf16(c["res"])[rows]
+    r, y = _new(T, H), _new(T, H)
+    _run(c, T, H, r, y, x=x, res=res)
+    want = [dev_bf16(bf16(v))[rows] for v in (r32, y32)]
+    assert torch.equal(r, want[0]) and torch.equal(y, want[1])
+
+
+def test_a_gate_group_goes_on_over_launches():
+    T, H, group = (1 << 21) + 700, 8, 1000
+    c = _case(1, H, 15, nv.NORM_RMS, False, None, False)
+    gate = torch.rand(-(-T // group), H, device="cuda").to(torch.bfloat16)
+    x = torch.ones(T, H, device="cuda", dtype=torch.bfloat16)
+    r = _new(T, H)
+    nv.nvfp4_residual_norm(x, None, None, gate, group, None, 1.0, None, None, EPS, 0, r, None, None, None, None, T, H)
+    assert torch.equal(r, gate.repeat_interleave(group, 0)[:T])
+
+
 def test_rows_past_32_bit_offsets():
     # rows 2^30 + 8 elements apart: the last starts past 2^33 bytes
     T, H, ld = 5, 272, (1 << 30) + 8
