@@ -468,8 +468,8 @@ typedef enum {
  * workspace: nvfp4_gemm_epilogue_workspace_size(M, N, K) bytes, under the
  * rules of nvfp4_gemm (zero-filled once, calls sharing it ordered on one
  * stream: two captured graphs that share it must not run at the same time).
- * ERR_SHAPE for an unknown act or a stride below N; ERR_UNSUPPORTED when M N is
- * past 2^35 (M rounded up to 16, N to 16).
+ * ERR_SHAPE for an unknown act or a stride below N; ERR_UNSUPPORTED for
+ * 2^24 tiles of 64 x 32 outputs or more (M N of about 2^35).
  */
 nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
                                  const float* alpha, const uint16_t* bias, int32_t act, const uint16_t* residual,

@@ -185,18 +185,14 @@ struct Call {
       stream = PyLong_AsVoidPtr(args[stream_arg]);
       if (PyErr_Occurred()) return nullptr;
     }
+    if (args[stream_arg] == Py_None && device >= 0)
+      stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
     int status;
-    try {
-      const bool current = args[stream_arg] == Py_None;
-      if (device >= 0 && device != c10::hip::current_device()) {
-        const c10::DeviceGuard guard(on);
-        status = call(current ? (void*)c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream() : stream);
-      } else {
-        status = call(current && device >= 0 ? (void*)c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream() : stream);
-      }
-    } catch (const std::exception& e) {
-      PyErr_SetString(PyExc_RuntimeError, e.what());
-      return nullptr;
+    if (device >= 0 && device != c10::hip::current_device()) {
+      const c10::DeviceGuard guard(on);
+      status = call(stream);
+    } else {
+      status = call(stream);
     }
     if (status != 0) {
       refuse(status, g_last_error());
@@ -207,7 +203,7 @@ struct Call {
 };
 
 // (a, a_sf, b, b_sf, alpha, bias, act, residual, beta, d, M, N, K, workspace, stream)
-PyObject* gemm_epilogue(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+PyObject* gemm_epilogue(PyObject* const* args, Py_ssize_t nargs) {
   Call c("nvfp4_gemm_epilogue", args, nargs, 15);
   if (c.failed) return nullptr;
   const int64_t M = c.integer(10), N = c.integer(11), K = c.integer(12);
@@ -228,7 +224,7 @@ PyObject* gemm_epilogue(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 }
 
 // (a, a_sf, b, b_sf, alpha, bias, act, h, M, I, K, workspace, stream)
-PyObject* gemm_gated(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+PyObject* gemm_gated(PyObject* const* args, Py_ssize_t nargs) {
   Call c("nvfp4_gemm_gated", args, nargs, 13);
   if (c.failed) return nullptr;
   const int64_t M = c.integer(8), I = c.integer(9), K = c.integer(10);
@@ -245,7 +241,7 @@ PyObject* gemm_gated(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 }
 
 // (a, a_sf, b, b_sf, alpha, bias, act, gs, q, sf, M, I, K, workspace, stream)
-PyObject* gemm_gated_quantize(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+PyObject* gemm_gated_quantize(PyObject* const* args, Py_ssize_t nargs) {
   Call c("nvfp4_gemm_gated_quantize", args, nargs, 15);
   if (c.failed) return nullptr;
   const int64_t M = c.integer(10), I = c.integer(11), K = c.integer(12);
@@ -264,7 +260,7 @@ PyObject* gemm_gated_quantize(PyObject*, PyObject* const* args, Py_ssize_t nargs
 
 // (a, a_sf, w_gu, w_gu_sf, alpha_gu, bias_gu, act, gs_h, w_d, w_d_sf, alpha_d, bias_d, residual, beta, d, M, H, I,
 //  workspace, stream)
-PyObject* ffn(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+PyObject* ffn(PyObject* const* args, Py_ssize_t nargs) {
   Call c("nvfp4_ffn", args, nargs, 20);
   if (c.failed) return nullptr;
   const int64_t M = c.integer(15), H = c.integer(16), I = c.integer(17);
@@ -288,7 +284,7 @@ PyObject* ffn(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 }
 
 // (x, post_weight, post_bias, gate, gate_group, residual, beta, weight, bias, eps, kind, r, y, gs, q, sf, T, H, stream)
-PyObject* residual_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+PyObject* residual_norm(PyObject* const* args, Py_ssize_t nargs) {
   Call c("nvfp4_residual_norm", args, nargs, 19);
   if (c.failed) return nullptr;
   const int64_t T = c.integer(16), H = c.integer(17), group = c.integer(4);
@@ -310,7 +306,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 }
 
 // setup(error class, last_error, epilogue, gated, gated_quantize, ffn, norm): addresses as integers
-PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+PyObject* setup(PyObject* const* args, Py_ssize_t nargs) {
   if (nargs != 7) {
     PyErr_SetString(PyExc_TypeError, "setup takes 7 arguments");
     return nullptr;
@@ -332,13 +328,27 @@ PyObject* setup(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   Py_RETURN_NONE;
 }
 
+// A Python entry point: no C++ exception leaves it (torch throws for tensors
+// without storage, sparse ones for instance).
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  try {
+    return F(args, nargs);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {
+    PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+  }
+  return nullptr;
+}
+
 PyMethodDef kMethods[] = {
-    {"setup", (PyCFunction)(void (*)())setup, METH_FASTCALL, nullptr},
-    {"gemm_epilogue", (PyCFunction)(void (*)())gemm_epilogue, METH_FASTCALL, nullptr},
-    {"gemm_gated", (PyCFunction)(void (*)())gemm_gated, METH_FASTCALL, nullptr},
-    {"gemm_gated_quantize", (PyCFunction)(void (*)())gemm_gated_quantize, METH_FASTCALL, nullptr},
-    {"ffn", (PyCFunction)(void (*)())ffn, METH_FASTCALL, nullptr},
-    {"residual_norm", (PyCFunction)(void (*)())residual_norm, METH_FASTCALL, nullptr},
+    {"setup", (PyCFunction)(void (*)())entry<setup>, METH_FASTCALL, nullptr},
+    {"gemm_epilogue", (PyCFunction)(void (*)())entry<gemm_epilogue>, METH_FASTCALL, nullptr},
+    {"gemm_gated", (PyCFunction)(void (*)())entry<gemm_gated>, METH_FASTCALL, nullptr},
+    {"gemm_gated_quantize", (PyCFunction)(void (*)())entry<gemm_gated_quantize>, METH_FASTCALL, nullptr},
+    {"ffn", (PyCFunction)(void (*)())entry<ffn>, METH_FASTCALL, nullptr},
+    {"residual_norm", (PyCFunction)(void (*)())entry<residual_norm>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", "Argument marshalling of the block operators.", -1, kMethods,

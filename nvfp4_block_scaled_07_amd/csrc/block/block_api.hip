@@ -22,12 +22,11 @@ bool stride_ok(int64_t* ld, int64_t cols) {
   return *ld >= cols;
 }
 
-// M N <= 2^35: tiles (16 x 16 outputs at least) times splits (16 at most) can
-// be counted in 31 bits.
+// Fewer than 2^24 tiles of 64 x 32 outputs (M N up to about 2^35): a launch has
+// fewer than 2^32 threads.
 bool sizes_ok(int64_t M, int64_t N) {
-  const int64_t kMax = int64_t(1) << 40;
-  if (M > kMax || N > kMax) return false;
-  return ((M + 15) / 16) <= (int64_t(1) << 31) / ((N + 15) / 16 * 16);
+  const int64_t kMax = int64_t(1) << 36;
+  return M <= kMax && N <= kMax && (M + 63) / 64 < (int64_t(1) << 24) / ((N + 31) / 32);
 }
 
 // The checks shared by the GEMM entry points; cols are the output columns and
@@ -51,7 +50,7 @@ nvfp4_status check_gemm(const char* fn, const void* a, const void* a_sf, const v
   if (!aligned(alpha, 4) || !aligned(bias, 2))
     return fail(NVFP4_ERR_ALIGN, "%s: alpha must be 4-byte and bias 2-byte aligned", fn);
   if (!sizes_ok(M, cols))
-    return fail(NVFP4_ERR_UNSUPPORTED, "%s: %lld x %lld outputs: at most 2^35 are supported", fn, (long long)M, (long long)cols);
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: %lld x %lld outputs: fewer than 2^24 tiles of 64 x 32 are supported", fn, (long long)M, (long long)cols);
   return NVFP4_OK;
 }
 

@@ -119,7 +119,7 @@ def test_queries():
     assert nv.nvfp4_gemm_gated_plan(1, 2048, 6144).startswith("gatedreg16x16")
     assert nv.nvfp4_gemm_gated_plan(8192, 8192, 6144).startswith("gated256x128")
     for f in (nv.nvfp4_gemm_epilogue_plan, nv.nvfp4_gemm_gated_plan):
-        assert f(16, 16, 100) == "none" and f(0, 16, 256) == "none" and f(1 << 22, 1 << 22, 256) == "none"
+        assert f(16, 16, 100) == "none" and f(0, 16, 256) == "none" and f(1 << 22, 1 << 22, 256) == "none" and f(1 << 30, 32, 256) == "none"
     assert nv.nvfp4_gemm_gated_workspace_size(-1, 16, 256) == 0
 
 

@@ -195,3 +195,49 @@ def test_graph_replays_and_another_stream():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(d, want), f"replay {i}"
+
+
+def test_refused_tensors_leave_the_output_alone():
+    M, N, K = 4, 32, 256
+    ops, *_ = _case(M, N, K, 5, False, False)
+    d = torch.full((M, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    call = lambda *a, **k: nv.nvfp4_gemm_epilogue(*a, **k)
+    base = [*ops, None, None, 0, None, 0.0, d, M, N, K]
+    half = torch.zeros(M, N, dtype=torch.float16, device="cuda")
+    wide = torch.zeros(M, 2 * N, dtype=torch.bfloat16, device="cuda")
+    bad = [(0, ops[0].cpu()), (0, ops[0][:2]), (2, ops[2].t()), (4, half.double()), (5, half[0]), (7, half), (9, half),
+           (7, wide), (9, wide[:, ::2]), (9, d[:3]), (9, d.t()), (9, d[:1].expand(M, N)), (9, np.zeros((M, N))),
+           (7, torch.zeros(M, N, device="meta", dtype=torch.bfloat16)), (6, 17), (10, -4)]
+    for i, v in bad:
+        args = list(base)
+        args[i] = v
+        with pytest.raises(nv.Nvfp4Error):
+            call(*args)
+    # a tensor without storage raises, it does not end the process
+    with pytest.raises((nv.Nvfp4Error, RuntimeError)):
+        call(*[d.to_sparse() if i == 9 else v for i, v in enumerate(base)])
+    for args in ([*base[:-1], "256"], [*base[:8], "x", *base[9:]]):
+        with pytest.raises(TypeError):
+            call(*args)
+    torch.cuda.synchronize()
+    assert (d == 3.0).all()
+
+
+def test_two_calls_at_once_on_two_streams():
+    M, N, K = 64, 768, 6144
+    cases = [_case(M, N, K, s, True, True) for s in (71, 72)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    args, want, got = [], [], []
+    for ops, _, _, bv, rv in cases:
+        args.append((*ops, scalar(ALPHA), dev_bf16(bv), nv.ACT_GELU, dev_bf16(rv), 1.0))
+        want.append(nv.nvfp4_gemm_epilogue(*args[-1], torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), M, N, K,
+                                           nv.gemm_epilogue_workspace(M, N, K)))
+        got.append(torch.empty(M, N, dtype=torch.bfloat16, device="cuda"))
+    spaces = [nv.gemm_epilogue_workspace(M, N, K) for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, s, d, ws in zip(args, streams, got, spaces):
+            nv.nvfp4_gemm_epilogue(*a, d, M, N, K, ws, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for d, w in zip(got, want):
+        assert torch.equal(d, w)
