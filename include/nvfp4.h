@@ -427,7 +427,9 @@ const char* nvfp4_mx_gemm_plan(int64_t M, int64_t N, int64_t K);
  * nvfp4_mx_gemm, 2 = the grouped GEMMs (kinds 0..3: per-wave dequantisation,
  * shared f16 A tile, 32-row and 64-row register kernels; the packed and fused
  * calls take kind 3 as 64-row passes and anything else as 32-row passes).
- * kind < 0 restores the library's choice.  The plan and workspace queries
+ * family 0 also steers the GEMMs with a fused epilogue below, where they have
+ * the kind: 9..12, 14..16 and 32 (16 x 32 register tiles); gated 9, 10, 12, 14, 15
+ * and 32.  kind < 0 restores the library's choice.  The plan and workspace queries
  * follow the override.  Not synchronised with calls in flight on other
  * threads: set it while no call of the family is being made.  ERR_SHAPE for
  * an unknown family or out-of-range kind or splits (> 16).
@@ -476,7 +478,7 @@ nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a, const uint8_t* a_sf, const ui
                                  int64_t ldr, float beta, uint16_t* d, int64_t ldd, int64_t M, int64_t N, int64_t K,
                                  void* workspace, size_t workspace_bytes, void* stream);
 size_t nvfp4_gemm_epilogue_workspace_size(int64_t M, int64_t N, int64_t K);
-/* Name of the plan (static string): those of nvfp4_gemm. */
+/* Name of the plan (static string). */
 const char* nvfp4_gemm_epilogue_plan(int64_t M, int64_t N, int64_t K);
 
 /*

@@ -9,6 +9,8 @@
 // fp32 or bf16 sums that separate kernels would make (2 to 6 bytes an element
 // and one launch each).  A gated tile takes the same columns of G and U, so
 // each product is formed where both factors are.
+#include <algorithm>
+
 #include "epilogue_tile.h"
 
 namespace nvfp4 {
@@ -17,14 +19,21 @@ typedef Cfg<64, 64, 1, 1, 32, 256, 2, 0, 4, 4> EpiTile64k4;
 typedef Cfg<128, 128, 2, 2, 32, 256, 2, 0, 1, 2> EpiTile128;
 typedef Cfg<64, 64, 1, 1, 32, 256, 2, 0, 4, 4, 16, 0, 0, 1> GatedTile64k4;  // 32 gate and 32 up columns
 typedef Cfg<128, 128, 2, 2, 32, 256, 2, 0, 1, 2, 16, 0, 0, 1> GatedTile128;
-typedef KCfg<16, 16, 4, 3, 4> EpiReg16x16;
-typedef KCfg<32, 16, 4, 3, 4> EpiReg32x16;
-typedef KCfg<32, 32, 4, 3, 2> EpiReg32x32;
-typedef KCfg<16, 32, 4, 3, 3> EpiReg16x32;
-typedef KCfg<16, 32, 8, 2, 2> EpiReg16x32k8;
-typedef KCfg<16, 32, 4, 3, 2, 0, 1> GatedReg16x16;  // 16 gate and 16 up columns
-typedef KCfg<16, 64, 4, 2, 2, 0, 1> GatedReg16x32;
-typedef KCfg<32, 32, 4, 3, 2, 0, 1> GatedReg32x16;
+// Register tiles of 8 waves with one K unit each in flight: a CU that gets one
+// work-group has two waves per SIMD, so one dequantises while the other waits
+// for its unit.  4 waves of three units in flight, the plain GEMM's shape, keep
+// as many bytes in flight in fewer waves (128 x 2048 x 2048: 8.6 us against 7.6;
+// 64 x 2048 x 2048 6.9 against 5.8; 1 x 768 x 2048 4.2 against 3.6; 1 x 16384 x
+// 2048 8.9 against 7.5), 8 waves of two or three units were no faster than 4
+// (8.5 and 9.8 at the first of these), 16 waves of one between (1 x 768 x 2048
+// 4.0).
+typedef KCfg<16, 16, 8, 1, 4> EpiReg16x16;
+typedef KCfg<16, 32, 8, 1, 4> EpiReg16x32;
+typedef KCfg<32, 16, 8, 1, 4> EpiReg32x16;
+typedef KCfg<32, 32, 8, 1, 4> EpiReg32x32;
+typedef KCfg<16, 32, 8, 1, 4, 0, 1> GatedReg16x16;  // 16 gate and 16 up columns
+typedef KCfg<16, 64, 8, 1, 4, 0, 1> GatedReg16x32;
+typedef KCfg<32, 32, 8, 1, 4, 0, 1> GatedReg32x16;
 
 // Register-streamed tile with a fused epilogue (small M).  What the epilogue
 // reads besides the sums (alpha, bias, residual) is loaded before the main
@@ -33,10 +42,10 @@ typedef KCfg<32, 32, 4, 3, 2, 0, 1> GatedReg32x16;
 // outputs, 16 consecutive lanes 16 columns of a row: one NVFP4 block.
 //
 // SKIP leaves the products of K units past the end of a wave's share out
-// instead of adding zeros (one token 6144 x 2048: 5.7 us against 6.3, 61 x 777 x
-// 1280: 4.4 against 5.0); where every slot is filled its branches only cut the
-// instruction schedule (1 x 4096 x 6144: 7.5 against 7.05), so the launcher
-// picks by the shape.
+// instead of adding zeros (1 x 6144 x 2304: 5.7 us against 6.1; 128 x 2048 x 2816:
+// 8.2 against 9.0; gated 16 x 2048 x 6144, split in two: 8.8 against 9.4); where
+// every slot is filled its branches only cut the instruction schedule (1 x 6144
+// x 2048: 5.04 against 4.95), so the launcher picks by the shape.
 template <class C, bool QUANT, bool SKIP>
 __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::OCC))) void k_gemm_kreg_epilogue(
     EpilogueLaunch p) {
@@ -147,10 +156,59 @@ static void launch_kreg_epilogue(const EpilogueLaunch& p, unsigned grid, hipStre
     hipLaunchKernelGGL((k_gemm_kreg_epilogue<C, QUANT, true>), dim3(grid), dim3(C::kThreads), 0, stream, p);
 }
 
-// Plan kinds that only the block GEMMs have, numbered past the plain GEMM's.
-static constexpr int kReg16x32 = 32, kReg16x32k8 = 33;
-static const PlanKind kEpi32 = {"kreg16x32", 16, 32, 256, true, true, false, EpiReg16x32::KS, EpiReg16x32::D};
-static const PlanKind kEpi33 = {"kreg16x32k8", 16, 32, 256, true, true, false, EpiReg16x32k8::KS, EpiReg16x32k8::D};
+// Plan kinds, numbered like the plain GEMM's kinds of the same tile; bn is the
+// output columns of a tile (a gated tile's B has twice as many).
+static constexpr int kReg16x32 = 32;  // a tile that only the block GEMMs have
+struct BlockKind {
+  int kind;
+  PlanKind k;
+};
+static const BlockKind kEpiKinds[] = {
+    {9, {"tile64x64k4", 64, 64, 256, true, false, false, 4}},
+    {10, {"kreg16x16k8", 16, 16, 256, true, true, false, EpiReg16x16::KS, EpiReg16x16::D}},
+    {11, {"kreg32x16k8", 32, 16, 256, true, true, false, EpiReg32x16::KS, EpiReg32x16::D}},
+    {12, {"kreg32x32k8", 32, 32, 256, true, true, false, EpiReg32x32::KS, EpiReg32x32::D}},
+    {kReg16x32, {"kreg16x32k8", 16, 32, 256, true, true, false, EpiReg16x32::KS, EpiReg16x32::D}}};
+static const BlockKind kGatedKinds[] = {
+    {9, {"gated64x32k4", 64, 32, 256, true, false, false, 4}},
+    {10, {"gatedreg16x16k8", 16, 16, 256, true, true, false, GatedReg16x16::KS, GatedReg16x16::D}},
+    {12, {"gatedreg32x16k8", 32, 16, 256, true, true, false, GatedReg32x16::KS, GatedReg32x16::D}},
+    {14, {"gated256x128w8", 256, 128, 256, false, false, false}},
+    {15, {"gated128x64", 128, 64, 256, false, false, false}},
+    {kReg16x32, {"gatedreg16x32k8", 16, 32, 256, true, true, false, GatedReg16x32::KS, GatedReg16x32::D}}};
+
+template <int N>
+static const PlanKind* find_kind(const BlockKind (&kinds)[N], int kind) {
+  for (const BlockKind& b : kinds)
+    if (b.kind == kind) return &b.k;
+  return nullptr;
+}
+
+static int64_t tiles_of(const PlanKind& k, int64_t M, int64_t cols) {
+  return ((M + k.bm - 1) / k.bm) * ((cols + k.bn - 1) / k.bn);
+}
+
+// Splits of the 64-row K-group tiles: up to three work-groups per CU and five
+// splits (as the plain GEMM), but each with about 5 stages at least, and the
+// number that fills the rounds of 256 work-groups best.  An exchange costs about
+// 2.5 us, four stages (333 x 2001 x 1536: 9.8 us unsplit, 12.7 in two; 1024 x 768 x
+// 2048 10.5 and 12.1; 256 x 768 x 6144 11.9 in five, 13.0 in three).
+static int tile_splits(int64_t tiles, int64_t K) {
+  const int64_t stages = K / 256;
+  int64_t most = std::min<int64_t>({3 * kCUs / tiles, 5, (stages + 1) / 5});
+  if (tiles >= 2 * kCUs || most < 1) most = 1;
+  int best = 1;
+  double best_fill = 0.0;
+  for (int s = 1; s <= most; ++s) {
+    const int64_t wgs = tiles * s, rounds = (wgs + kCUs - 1) / kCUs;
+    const double fill = (double)wgs / (double)(rounds * kCUs);
+    if (fill > best_fill || (fill == best_fill && stages >= 6 * s)) {
+      best = s;
+      best_fill = fill;
+    }
+  }
+  return best;
+}
 
 static GemmPlan plan_of(const PlanKind& k, int kind, int64_t M, int64_t cols, int64_t K, int forced_splits, bool gated) {
   GemmPlan pl;
@@ -159,6 +217,7 @@ static GemmPlan plan_of(const PlanKind& k, int kind, int64_t M, int64_t cols, in
   pl.tiles_m = (M + k.bm - 1) / k.bm;
   pl.tiles_n = (cols + k.bn - 1) / k.bn;
   pl.group_m = 8;
+  if (kind == 9 && forced_splits <= 0) forced_splits = tile_splits(pl.tiles_m * pl.tiles_n, K);
   if (!k.splitk || pl.tiles_m * pl.tiles_n > kCounterBytes / 4) forced_splits = 1;
   PlanKind both = k;  // a gated tile's partials hold both matrices' sums
   if (gated) both.bn *= 2;
@@ -166,68 +225,60 @@ static GemmPlan plan_of(const PlanKind& k, int kind, int64_t M, int64_t cols, in
   return pl;
 }
 
-// The plain epilogue runs the plain GEMM's plans (the epilogue adds no operand
-// traffic to the main loop), except up to M = 16, where 16 x 32 tiles take the
-// place of 32 x 32 ones, half of whose A rows would be empty: 8 waves with all
-// of up to 16 K units in flight at once while a CU gets one work-group, else 4
-// waves (16 x 6144 x 2048: 6.9 us against 8.1; 1 x 6144 x 2048: 6.4 against 7.4;
-// 16 x 6144 x 16384: 20.6 against 24.6; 16 x 16384 x 6144: 18.1 against 20.4).
-GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K) {
-  int fk = -1, fs = 0;
-  const bool forced = forced_plan(kForceGemm, &fk, &fs);
-  if (forced && fk == kReg16x32) return plan_of(kEpi32, fk, M, N, K, fs, false);
-  if (forced && fk == kReg16x32k8) return plan_of(kEpi33, fk, M, N, K, fs, false);
-  GemmPlan pl = choose_plan(M, N, K, kAutoKinds);
-  if (M <= 16 && pl.kind == 12 && !(forced && fk == 12)) {
-    if ((N + 31) / 32 <= kCUs) return plan_of(kEpi33, kReg16x32k8, M, N, K, 0, false);
-    return plan_of(kEpi32, kReg16x32, M, N, K, 0, false);
+// The smallest register tile (fewest steps per wave) that needs at most one
+// work-group per CU, where a long K counts as one work-group per 24 units (so
+// that it is split over that many, or gets a larger tile: 64 x 768 x 16384, 14.9
+// us on 16 x 16 tiles, 12.9 on 32 x 32; 128 x 768 x 16384 21.6 on 32 x 16, 16.5 on the
+// 64-row tiles); up to M = 16 16 x 32 tiles take over to four work-groups per CU
+// (16 x 16384 x 6144: 16.6 us; 64-row tiles 21).  -1: none of them; their one
+// wave per 16 or 32 columns then dequantises A too often.
+template <int N>
+static int register_kind(const BlockKind (&kinds)[N], int64_t M, int64_t cols, int64_t K) {
+  const int64_t work_groups = M <= 16 ? 1 : (K / 256 + 23) / 24;
+  for (int kind : {10, 11, 12}) {
+    const PlanKind* k = find_kind(kinds, kind);
+    if (k && tiles_of(*k, M, cols) * work_groups <= kCUs && (M > 16 || kind == 10)) return kind;
   }
-  if (pl.kind == 15) {  // never split by the plan's own rule; a forced split is not supported here
-    pl.splits = 1;
-    pl.workspace = 0;
-  }
-  return pl;
+  if (M <= 16 && tiles_of(*find_kind(kinds, kReg16x32), M, cols) <= 4 * kCUs) return kReg16x32;
+  return -1;
 }
 
-// Gated plans, numbered like the plain GEMM's kinds of the same shape; bn is
-// the output columns of a tile (its B has twice as many).
-static const PlanKind kGated14 = {"gated256x128w8", 256, 128, 256, false, false, false};
-static const PlanKind kGated15 = {"gated128x64", 128, 64, 256, false, false, false};
-static const PlanKind kGated9 = {"gated64x32k4", 64, 32, 256, true, false, false, 4};
-static const PlanKind kGated10 = {"gatedreg16x16", 16, 16, 256, true, true, false, GatedReg16x16::KS, GatedReg16x16::D};
-static const PlanKind kGated12 = {"gatedreg32x16", 32, 16, 256, true, true, false, GatedReg32x16::KS, GatedReg32x16::D};
-static const PlanKind kGated32 = {"gatedreg16x32", 16, 32, 256, true, true, false, GatedReg16x32::KS, GatedReg16x32::D};
-
-// From sweeps of M = 32..4096, I = 1024..16384, K = 2048 and 6144.  Register
-// tiles up to M = 128 while they need at most one work-group per CU; up to M =
-// 16 wider matrices take 16 x 32 register tiles (16 x 6144 x 2048 outputs: 8.6 us
-// against 11.9 for 32 x 16; 16 x 16384 x 6144: 30.6 against 38).  256-row tiles
-// (one work-group per CU) where their last round is at least 85% full in the
-// mean (2048 x 4096 x 6144, one full round: 163 us against 191 on 128-row
-// tiles; 1024 x 4096, half a round: 133 against 100), 128-row tiles from one
-// round of two work-groups per CU on (1024 x 4096 x 6144: 100 us against 108.5 on
-// 64-row tiles; half a round: 59 against 57), else split 64-row tiles.
-GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K) {
-  auto tiles = [&](const PlanKind& k) { return ((M + k.bm - 1) / k.bm) * ((I + k.bn - 1) / k.bn); };
-  const int64_t t14 = tiles(kGated14), rounds14 = (t14 + kCUs - 1) / kCUs;
-  int kind = 9;
-  if (M <= 128 && tiles(kGated10) <= kCUs) kind = 10;
-  else if (M <= 16 && tiles(kGated32) <= 4 * kCUs) kind = kReg16x32;
-  else if (M <= 128 && tiles(kGated12) <= kCUs) kind = 12;
-  else if (M > 64 && t14 * 100 >= rounds14 * kCUs * 85) kind = 14;
-  else if (M > 64 && tiles(kGated15) >= 2 * kCUs) kind = 15;
+// Register tiles, else the plain GEMM's plan (the epilogue adds no operand
+// traffic to the main loop) with the splits above.
+GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K) {
   int fk = -1, fs = 0;
-  auto has = [](int k) { return k == 9 || k == 10 || k == 12 || k == 14 || k == 15 || k == kReg16x32; };
-  if (forced_plan(kForceGemm, &fk, &fs) && has(fk)) kind = fk;
+  if (!forced_plan(kForceGemm, &fk, &fs)) fk = -1;
+  int kind = register_kind(kEpiKinds, M, N, K);
+  if (find_kind(kEpiKinds, fk)) kind = fk;
   else fs = 0;
-  switch (kind) {
-    case 10: return plan_of(kGated10, kind, M, I, K, fs, true);
-    case 12: return plan_of(kGated12, kind, M, I, K, fs, true);
-    case 14: return plan_of(kGated14, kind, M, I, K, fs, true);
-    case 15: return plan_of(kGated15, kind, M, I, K, fs, true);
-    case kReg16x32: return plan_of(kGated32, kind, M, I, K, fs, true);
-    default: return plan_of(kGated9, kind, M, I, K, fs, true);
+  if (kind < 0 || fk == 14 || fk == 15 || fk == 16) {
+    GemmPlan pl = choose_plan(M, N, K, kAutoKinds);
+    pl.splits = 1;  // the large tiles are not split here
+    pl.workspace = 0;
+    if (pl.kind >= 14) return pl;
+    kind = 9;
   }
+  return plan_of(*find_kind(kEpiKinds, kind), kind, M, N, K, fs, false);
+}
+
+// Gated plans, from sweeps of M = 1..4096, I = 768..16384, K = 1024..16384.
+// 256-row tiles (one work-group per CU) where their last round is at least 85%
+// full in the mean (2048 x 4096 x 6144, one full round: 163 us against 191 on
+// 128-row tiles; 1024 x 4096, half a round: 133 against 100), 128-row tiles from
+// one round of two work-groups per CU on (1024 x 4096 x 6144: 100 us against 108.5
+// on 64-row tiles; half a round: 59 against 57), else 64-row tiles.
+GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K) {
+  const int64_t t14 = tiles_of(*find_kind(kGatedKinds, 14), M, I), rounds14 = (t14 + kCUs - 1) / kCUs;
+  int kind = register_kind(kGatedKinds, M, I, K);
+  if (kind < 0) {
+    kind = 9;
+    if (M > 64 && t14 * 100 >= rounds14 * kCUs * 85) kind = 14;
+    else if (M > 64 && tiles_of(*find_kind(kGatedKinds, 15), M, I) >= 2 * kCUs) kind = 15;
+  }
+  int fk = -1, fs = 0;
+  if (forced_plan(kForceGemm, &fk, &fs) && find_kind(kGatedKinds, fk)) kind = fk;
+  else fs = 0;
+  return plan_of(*find_kind(kGatedKinds, kind), kind, M, I, K, fs, true);
 }
 
 hipError_t launch_gemm_epilogue(const GemmPlan& pl, EpilogueLaunch p, hipStream_t stream) {
@@ -241,7 +292,6 @@ hipError_t launch_gemm_epilogue(const GemmPlan& pl, EpilogueLaunch p, hipStream_
     case 11: launch_kreg_epilogue<EpiReg32x16, false>(p, grid, stream); break;
     case 12: launch_kreg_epilogue<EpiReg32x32, false>(p, grid, stream); break;
     case kReg16x32: launch_kreg_epilogue<EpiReg16x32, false>(p, grid, stream); break;
-    case kReg16x32k8: launch_kreg_epilogue<EpiReg16x32k8, false>(p, grid, stream); break;
     case 14:
     case 16: launch_epilogue_large(pl.kind, p, grid, stream); break;
     case 15: launch_epilogue_tile<EpiTile128, false>(p, grid, stream); break;

@@ -65,9 +65,9 @@ def test_epilogue_refusals():
     assert _epi(ldd=15) == SHAPE and "ldd" in nv.nvfp4_last_error()
     assert _epi(residual=FAKE, ldr=15) == SHAPE and "ldr" in nv.nvfp4_last_error()
     assert _epi(residual=FAKE, ldr=-1) == SHAPE
-    need = nv.nvfp4_gemm_epilogue_workspace_size(1024, 256, 6144)
+    need = nv.nvfp4_gemm_epilogue_workspace_size(1024, 768, 6144)
     assert need > 0
-    shape = dict(M=1024, N=256, K=6144)
+    shape = dict(M=1024, N=768, K=6144)
     assert _epi(**shape) == WORKSPACE and "workspace" in nv.nvfp4_last_error()
     assert _epi(**shape, ws=FAKE, wsb=need - 1) == WORKSPACE
     assert _epi(**shape, ws=FAKE + 16, wsb=need) == ALIGN
@@ -113,9 +113,16 @@ def test_norm_refusals():
 
 
 def test_queries():
-    for M, N, K in [(1, 768, 6144), (64, 2048, 6144), (1024, 768, 6144), (8192, 6144, 6144)]:
+    for M, N, K in [(8192, 6144, 6144), (2048, 6144, 16384), (4096, 4096, 6144)]:
         assert nv.nvfp4_gemm_epilogue_plan(M, N, K) == nv.nvfp4_gemm_plan(M, N, K)
-        assert nv.nvfp4_gemm_epilogue_workspace_size(M, N, K) == nv.nvfp4_gemm_workspace_size(M, N, K)
+        assert nv.nvfp4_gemm_epilogue_workspace_size(M, N, K) == nv.nvfp4_gemm_workspace_size(M, N, K) == 0
+    for (M, N, K), plan in {(1, 768, 6144): "kreg16x16k8", (16, 6144, 2048): "kreg16x32k8", (64, 2048, 6144): "kreg32x16k8",
+                            (256, 1024, 2048): "kreg32x32k8", (64, 768, 16384): "kreg32x32k8",
+                            (128, 768, 16384): "tile64x64k4", (1024, 768, 6144): "tile64x64k4"}.items():
+        assert nv.nvfp4_gemm_epilogue_plan(M, N, K) == plan, (M, N, K)
+    # one split, its counters, or partials of S tiles behind 4096 bytes of counters
+    assert nv.nvfp4_gemm_epilogue_workspace_size(333, 2001, 1536) == 0
+    assert nv.nvfp4_gemm_epilogue_workspace_size(1024, 768, 6144) == 4096 + 192 * 4 * 64 * 64 * 4
     assert nv.nvfp4_gemm_gated_plan(1, 2048, 6144).startswith("gatedreg16x16")
     assert nv.nvfp4_gemm_gated_plan(8192, 8192, 6144).startswith("gated256x128")
     for f in (nv.nvfp4_gemm_epilogue_plan, nv.nvfp4_gemm_gated_plan):
