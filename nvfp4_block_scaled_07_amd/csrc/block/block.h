@@ -26,7 +26,7 @@ struct EpilogueLaunch {
 };
 
 GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K);
-GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K);
+GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K, bool quantize);
 hipError_t launch_gemm_epilogue(const GemmPlan& plan, EpilogueLaunch p, hipStream_t stream);
 // quantize: NVFP4 output instead of bf16 (cols % 16 == 0)
 hipError_t launch_gemm_gated(const GemmPlan& plan, EpilogueLaunch p, bool quantize, hipStream_t stream);

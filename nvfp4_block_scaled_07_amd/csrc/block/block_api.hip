@@ -1,6 +1,8 @@
 // C entry points of the block operators: host-side validation, plan choice
 // and launch.  As everywhere in the library, every check runs on the host
 // before anything is enqueued.
+#include <algorithm>
+
 #include "../api_util.h"
 #include "block.h"
 
@@ -131,11 +133,12 @@ nvfp4_status nvfp4_gemm_epilogue(const uint8_t* a, const uint8_t* a_sf, const ui
 }
 
 size_t nvfp4_gemm_gated_workspace_size(int64_t M, int64_t I, int64_t K) {
-  return gemm_sizes(M, I, K) ? nvfp4::choose_gated_plan(M, I, K).workspace : 0;
+  if (!gemm_sizes(M, I, K)) return 0;
+  return std::max(nvfp4::choose_gated_plan(M, I, K, false).workspace, nvfp4::choose_gated_plan(M, I, K, true).workspace);
 }
 
 const char* nvfp4_gemm_gated_plan(int64_t M, int64_t I, int64_t K) {
-  return gemm_sizes(M, I, K) ? nvfp4::choose_gated_plan(M, I, K).name : "none";
+  return gemm_sizes(M, I, K) ? nvfp4::choose_gated_plan(M, I, K, false).name : "none";
 }
 
 nvfp4_status nvfp4_gemm_gated(const uint8_t* a, const uint8_t* a_sf, const uint8_t* b, const uint8_t* b_sf,
@@ -149,7 +152,7 @@ nvfp4_status nvfp4_gemm_gated(const uint8_t* a, const uint8_t* a_sf, const uint8
   if (!h) return fail(NVFP4_ERR_NULL, "%s: h must not be NULL", fn);
   if (!aligned(h, 2)) return fail(NVFP4_ERR_ALIGN, "%s: h must be 2-byte aligned", fn);
   if (!stride_ok(&ldh, I)) return fail(NVFP4_ERR_SHAPE, "%s: ldh = %lld is below I = %lld", fn, (long long)ldh, (long long)I);
-  const GemmPlan plan = nvfp4::choose_gated_plan(M, I, K);
+  const GemmPlan plan = nvfp4::choose_gated_plan(M, I, K, false);
   if ((s = check_workspace(fn, workspace, workspace_bytes, plan.workspace)) != NVFP4_OK) return s;
   EpilogueLaunch p = launch_of(a, a_sf, b, b_sf, alpha, bias, act, M, 2 * I, I, K, workspace);
   p.g.d = h;
@@ -168,7 +171,7 @@ nvfp4_status nvfp4_gemm_gated_quantize(const uint8_t* a, const uint8_t* a_sf, co
   if (s != NVFP4_OK || empty) return s;
   if (!q || !sf) return fail(NVFP4_ERR_NULL, "%s: q and sf must not be NULL", fn);
   if (!aligned(q, 8) || !aligned(gs, 4)) return fail(NVFP4_ERR_ALIGN, "%s: q must be 8-byte and gs 4-byte aligned", fn);
-  const GemmPlan plan = nvfp4::choose_gated_plan(M, I, K);
+  const GemmPlan plan = nvfp4::choose_gated_plan(M, I, K, true);
   if ((s = check_workspace(fn, workspace, workspace_bytes, plan.workspace)) != NVFP4_OK) return s;
   EpilogueLaunch p = launch_of(a, a_sf, b, b_sf, alpha, bias, act, M, 2 * I, I, K, workspace);
   p.gs = gs;
@@ -189,7 +192,7 @@ struct FfnSpace {
 
 FfnSpace ffn_space(int64_t M, int64_t H, int64_t I) {
   FfnSpace f;
-  f.gated = nvfp4::choose_gated_plan(M, I, H);
+  f.gated = nvfp4::choose_gated_plan(M, I, H, true);
   f.down = nvfp4::choose_epilogue_plan(M, H, I);
   size_t split = 4096;
   if (f.gated.workspace > split) split = f.gated.workspace;

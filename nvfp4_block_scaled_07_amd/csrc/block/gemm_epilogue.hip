@@ -33,6 +33,7 @@ typedef KCfg<32, 16, 8, 1, 4> EpiReg32x16;
 typedef KCfg<32, 32, 8, 1, 4> EpiReg32x32;
 typedef KCfg<16, 32, 8, 1, 4, 0, 1> GatedReg16x16;  // 16 gate and 16 up columns
 typedef KCfg<16, 64, 8, 1, 4, 0, 1> GatedReg16x32;
+typedef KCfg<16, 16, 8, 1, 4, 0, 2> GatedReg16x8;   // 8 and 8
 typedef KCfg<32, 32, 8, 1, 4, 0, 1> GatedReg32x16;
 
 // Register-streamed tile with a fused epilogue (small M).  What the epilogue
@@ -52,9 +53,12 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
   __shared__ __attribute__((aligned(16))) float red[C::KS * C::kTileFloats];
   __shared__ int last_flag;
   constexpr bool kGated = C::kGated;
-  constexpr int kCols = C::kBlkN * 16;  // output columns of the tile
+  constexpr int kCols = kGated ? C::BN / 2 : C::BN;  // output columns of the tile
   constexpr int kOut = C::BM * kCols, kPer = (kOut + C::kThreads - 1) / C::kThreads;
-  static_assert(kCols % 16 == 0, "whole NVFP4 blocks in a row of lanes");
+  static_assert(!QUANT || kCols % 16 == 0, "whole NVFP4 blocks in a row of lanes");
+  // tile columns of output column c
+  auto gate_col = [](int c) { return C::kHalves ? c / 8 * 16 + c % 8 : c; };
+  auto up_col = [](int c) { return C::kHalves ? c / 8 * 16 + c % 8 + 8 : kCols + c; };
   const int tiles_n = (int)p.g.tiles_n, S = p.g.splits;
   const int L = xcd_remap(blockIdx.x, (int)(p.g.tiles_m * p.g.tiles_n) * S);
   // uniform shortcuts past the integer divisions (about 100 cycles each) for
@@ -125,8 +129,8 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
   for (int k = 0; k < kPer; ++k) {
     const int x = threadIdx.x + k * C::kThreads, row = x / kCols, col = x % kCols;
     if (x >= kOut) break;
-    s0[k] = total(row, col);
-    s1[k] = kGated ? total(row, kCols + col) : 0.0f;
+    s0[k] = total(row, gate_col(col));
+    s1[k] = kGated ? total(row, up_col(col)) : 0.0f;
   }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -158,7 +162,7 @@ static void launch_kreg_epilogue(const EpilogueLaunch& p, unsigned grid, hipStre
 
 // Plan kinds, numbered like the plain GEMM's kinds of the same tile; bn is the
 // output columns of a tile (a gated tile's B has twice as many).
-static constexpr int kReg16x32 = 32;  // a tile that only the block GEMMs have
+static constexpr int kReg16x32 = 32, kReg16x8 = 33;  // tiles that only the block GEMMs have
 struct BlockKind {
   int kind;
   PlanKind k;
@@ -175,6 +179,7 @@ static const BlockKind kGatedKinds[] = {
     {12, {"gatedreg32x16k8", 32, 16, 256, true, true, false, GatedReg32x16::KS, GatedReg32x16::D}},
     {14, {"gated256x128w8", 256, 128, 256, false, false, false}},
     {15, {"gated128x64", 128, 64, 256, false, false, false}},
+    {kReg16x8, {"gatedreg16x8k8", 16, 8, 256, true, true, false, GatedReg16x8::KS, GatedReg16x8::D}},
     {kReg16x32, {"gatedreg16x32k8", 16, 32, 256, true, true, false, GatedReg16x32::KS, GatedReg16x32::D}}};
 
 template <int N>
@@ -210,6 +215,28 @@ static int tile_splits(int64_t tiles, int64_t K) {
   return best;
 }
 
+// Splits of the register tiles: the least estimated time, of the K units of a
+// wave (proportional to the rows of A and B that a unit has: 1.3 us for 32 of
+// them) and the exchange (1.5 us and a little more per split), while every
+// work-group has a CU.  Cold, 16 x 256 x 6144 on 16 tiles of 16 x 16: 6.7, 6.3, 5.8,
+// 5.8 us in 1 to 4 splits; 1 x 768 x 6144 on 48: 5.3, 5.6, 5.4, 5.6; 16 x 768 x 2304,
+// one unit past a whole round: 4.4 unsplit, 5.2 in two; 32 x 32 tiles, 64 x 1024 x
+// 6144: 12.6, 10.5, 9.7, 9.5.
+static int register_splits(const PlanKind& k, int64_t M, int64_t tiles, int64_t b_rows, int64_t K) {
+  const double units = (double)(K / 256) / k.ks;
+  const double unit_us = 1.3 / 32 * (double)(std::min<int64_t>(M, k.bm) + b_rows);
+  int best = 1;
+  double least = units * unit_us;
+  for (int s = 2; s <= 8 && tiles * s <= kCUs && s <= K / 256; ++s) {
+    const double us = units / s * unit_us + 1.5 + 0.05 * s;
+    if (us < least) {
+      best = s;
+      least = us;
+    }
+  }
+  return best;
+}
+
 static GemmPlan plan_of(const PlanKind& k, int kind, int64_t M, int64_t cols, int64_t K, int forced_splits, bool gated) {
   GemmPlan pl;
   pl.kind = kind;
@@ -217,10 +244,11 @@ static GemmPlan plan_of(const PlanKind& k, int kind, int64_t M, int64_t cols, in
   pl.tiles_m = (M + k.bm - 1) / k.bm;
   pl.tiles_n = (cols + k.bn - 1) / k.bn;
   pl.group_m = 8;
-  if (kind == 9 && forced_splits <= 0) forced_splits = tile_splits(pl.tiles_m * pl.tiles_n, K);
-  if (!k.splitk || pl.tiles_m * pl.tiles_n > kCounterBytes / 4) forced_splits = 1;
   PlanKind both = k;  // a gated tile's partials hold both matrices' sums
   if (gated) both.bn *= 2;
+  const int64_t tiles = pl.tiles_m * pl.tiles_n;
+  if (!k.splitk || tiles > kCounterBytes / 4) forced_splits = 1;
+  else if (forced_splits <= 0) forced_splits = k.kreg ? register_splits(k, M, tiles, both.bn, K) : tile_splits(tiles, K);
   plan_splits(pl, both, K, forced_splits);
   return pl;
 }
@@ -229,15 +257,20 @@ static GemmPlan plan_of(const PlanKind& k, int kind, int64_t M, int64_t cols, in
 // work-group per CU, where a long K counts as one work-group per 24 units (so
 // that it is split over that many, or gets a larger tile: 64 x 768 x 16384, 14.9
 // us on 16 x 16 tiles, 12.9 on 32 x 32; 128 x 768 x 16384 21.6 on 32 x 16, 16.5 on the
-// 64-row tiles); up to M = 16 16 x 32 tiles take over to four work-groups per CU
-// (16 x 16384 x 6144: 16.6 us; 64-row tiles 21).  -1: none of them; their one
-// wave per 16 or 32 columns then dequantises A too often.
+// 64-row tiles), per 20 for the largest where the 64-row tiles have full rows
+// (256 x 768 x 6144 13.3 us against 11.8); up to M = 16 16 x 16 tiles are split less, and 16 x 32 tiles take
+// over to four work-groups per CU (16 x 16384 x 6144: 16.6 us; 64-row tiles 21).
+// -1: none of them; their one wave per 16 or 32 columns then dequantises A too
+// often.
 template <int N>
-static int register_kind(const BlockKind (&kinds)[N], int64_t M, int64_t cols, int64_t K) {
-  const int64_t work_groups = M <= 16 ? 1 : (K / 256 + 23) / 24;
-  for (int kind : {10, 11, 12}) {
+static int register_kind(const BlockKind (&kinds)[N], int64_t M, int64_t cols, int64_t K, bool halves) {
+  const int64_t units = K / 256;
+  for (int kind : {kReg16x8, 10, 11, 12}) {
     const PlanKind* k = find_kind(kinds, kind);
-    if (k && tiles_of(*k, M, cols) * work_groups <= kCUs && (M > 16 || kind == 10)) return kind;
+    if (!k || (kind == kReg16x8 && !halves) || (M <= 16 && k->bm > 16)) continue;
+    const int64_t per = kind == 12 && M > 32 ? 20 : 24;
+    const int64_t work_groups = M <= 16 && kind == 10 ? 1 : (units + per - 1) / per;
+    if (tiles_of(*k, M, cols) * work_groups <= kCUs) return kind;
   }
   if (M <= 16 && tiles_of(*find_kind(kinds, kReg16x32), M, cols) <= 4 * kCUs) return kReg16x32;
   return -1;
@@ -248,7 +281,7 @@ static int register_kind(const BlockKind (&kinds)[N], int64_t M, int64_t cols, i
 GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K) {
   int fk = -1, fs = 0;
   if (!forced_plan(kForceGemm, &fk, &fs)) fk = -1;
-  int kind = register_kind(kEpiKinds, M, N, K);
+  int kind = register_kind(kEpiKinds, M, N, K, false);
   if (find_kind(kEpiKinds, fk)) kind = fk;
   else fs = 0;
   if (kind < 0 || fk == 14 || fk == 15 || fk == 16) {
@@ -261,22 +294,27 @@ GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K) {
   return plan_of(*find_kind(kEpiKinds, kind), kind, M, N, K, fs, false);
 }
 
+// halves: 16 x 8 tiles, 8 gate and 8 up rows in one block of columns, have enough
+// work-groups to leave K whole (one token, 2048 x 6144: 6.7 us against 8.2 on 16 x
+// 16 tiles in two splits); an NVFP4 block has 16 columns, so they are for bf16.
+//
 // Gated plans, from sweeps of M = 1..4096, I = 768..16384, K = 1024..16384.
 // 256-row tiles (one work-group per CU) where their last round is at least 85%
 // full in the mean (2048 x 4096 x 6144, one full round: 163 us against 191 on
 // 128-row tiles; 1024 x 4096, half a round: 133 against 100), 128-row tiles from
 // one round of two work-groups per CU on (1024 x 4096 x 6144: 100 us against 108.5
 // on 64-row tiles; half a round: 59 against 57), else 64-row tiles.
-GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K) {
+GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K, bool quantize) {
+  const bool halves = !quantize && I * (K / 16) < (int64_t(1) << 30);
   const int64_t t14 = tiles_of(*find_kind(kGatedKinds, 14), M, I), rounds14 = (t14 + kCUs - 1) / kCUs;
-  int kind = register_kind(kGatedKinds, M, I, K);
+  int kind = register_kind(kGatedKinds, M, I, K, halves);
   if (kind < 0) {
     kind = 9;
     if (M > 64 && t14 * 100 >= rounds14 * kCUs * 85) kind = 14;
     else if (M > 64 && tiles_of(*find_kind(kGatedKinds, 15), M, I) >= 2 * kCUs) kind = 15;
   }
   int fk = -1, fs = 0;
-  if (forced_plan(kForceGemm, &fk, &fs) && find_kind(kGatedKinds, fk)) kind = fk;
+  if (forced_plan(kForceGemm, &fk, &fs) && find_kind(kGatedKinds, fk) && (fk != kReg16x8 || halves)) kind = fk;
   else fs = 0;
   return plan_of(*find_kind(kGatedKinds, kind), kind, M, I, K, fs, true);
 }
@@ -306,6 +344,9 @@ static void launch_gated(const GemmPlan& pl, const EpilogueLaunch& p, unsigned g
     case 10: launch_kreg_epilogue<GatedReg16x16, QUANT>(p, grid, stream); break;
     case 12: launch_kreg_epilogue<GatedReg32x16, QUANT>(p, grid, stream); break;
     case kReg16x32: launch_kreg_epilogue<GatedReg16x32, QUANT>(p, grid, stream); break;
+    case kReg16x8:
+      if constexpr (!QUANT) launch_kreg_epilogue<GatedReg16x8, false>(p, grid, stream);
+      break;
     case 14: launch_gated_large(p, QUANT, grid, stream); break;
     case 15: launch_epilogue_tile<GatedTile128, QUANT>(p, grid, stream); break;
     default: launch_epilogue_tile<GatedTile64k4, QUANT>(p, grid, stream); break;

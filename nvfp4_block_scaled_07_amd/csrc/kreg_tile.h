@@ -93,21 +93,25 @@ struct SfLayout {
 // GATED tiles pair two weight matrices stored one after the other in B
 // ([N / 2] gate rows, then [N / 2] up rows): column blocks 0 .. TN / 2 - 1 of
 // the tile are gate rows n0 .., blocks TN / 2 .. TN - 1 the same up rows, so a
-// tile covers BN / 2 gate columns and holds the product's two factors.
+// tile covers BN / 2 gate columns and holds the product's two factors.  With
+// GATED 2 every column block holds 8 gate rows and the same 8 up rows instead
+// (the two whole-line loads of a block read 8 rows each as it is), for tiles
+// of 8 outputs; the scales of both matrices then lie in one descriptor, so
+// N K / 32 < 2^31.
 // ---------------------------------------------------------------------------
 template <int BM_, int BN_, int KS_, int D_, int OCC_, int MX_ = 0, int GATED_ = 0>
 struct KCfg {
-  static constexpr bool kGated = GATED_ != 0;
+  static constexpr bool kGated = GATED_ != 0, kHalves = GATED_ == 2;
   static constexpr int BM = BM_, BN = BN_, KS = KS_, D = D_, OCC = OCC_;
   static constexpr bool kMx = MX_ != 0;
   static constexpr int SBLK = kMx ? 32 : 16;        // elements per scale
   static constexpr int TM = BM / 16, TN = BN / 16;
-  static constexpr int kBlkN = kGated ? TN / 2 : TN;  // column blocks of one B matrix
+  static constexpr int kBlkN = GATED_ == 1 ? TN / 2 : TN;  // column blocks of one B matrix
   static constexpr int kThreads = KS * 64;
   static constexpr int kTileFloats = BM * BN;        // one wave's partial tile
   static constexpr int kUnit = 256;                  // K elements per unit
   static_assert(BM % 16 == 0 && BN % 16 == 0, "16-row MFMA blocks");
-  static_assert(!kGated || (TN % 2 == 0 && !kMx), "gated tiles pair NVFP4 column blocks");
+  static_assert(!kGated || ((TN % 2 == 0 || kHalves) && !kMx), "gated tiles pair NVFP4 column blocks");
   static_assert(KS >= 1 && KS <= 16, "waves per work-group");
   static_assert(KS * kTileFloats * 4 <= 65536, "partial tiles fit in 64 KB of LDS");
 };
@@ -144,7 +148,7 @@ __device__ __forceinline__ void kreg_load(KRegs<C>& R, int u, int unit, bool liv
   for (int tn = 0; tn < C::TN; ++tn) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const u4_t v = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(tn < C::kBlkN ? rb : rb2, live ? vb[tn][h] : kOut, so, 0));
+      const u4_t v = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(tn < C::kBlkN && !(C::kHalves && h) ? rb : rb2, live ? vb[tn][h] : kOut, so, 0));
 #pragma unroll
       for (int j = 0; j < 4; ++j) R.bq[u][tn][4 * h + j] = v[j];
     }
@@ -218,7 +222,8 @@ __device__ __forceinline__ void kreg_accumulate(const GemmLaunch& p, int64_t m0,
   const rsrc_t ra = make_rsrc(p.a + m0 * ld, (uint32_t)(rows_a * ld));
   const rsrc_t ras = SfLayout<SFL>::rsrc(p.a_sf, m0, rows_a, lds);
   const rsrc_t rb = make_rsrc(p.b + n0 * ld, (uint32_t)(rows_b * ld));
-  const rsrc_t rbs = SfLayout<SFL>::rsrc(p.b_sf, n0, rows_b, lds);
+  const rsrc_t rbs = C::kHalves ? make_rsrc(p.b_sf + n0 * lds, (uint32_t)((p.N / 2 + rows_b) * lds))
+                                : SfLayout<SFL>::rsrc(p.b_sf, n0, rows_b, lds);
   // the second matrix of a gated tile
   const int64_t n2 = C::kGated ? p.N / 2 + n0 : n0;
   const rsrc_t rb2 = C::kGated ? make_rsrc(p.b + n2 * ld, (uint32_t)(rows_b * ld)) : rb;
@@ -242,6 +247,13 @@ __device__ __forceinline__ void kreg_accumulate(const GemmLaunch& p, int64_t m0,
   }
 #pragma unroll
   for (int tn = 0; tn < C::TN; ++tn) {
+    if constexpr (C::kHalves) {
+      static_assert(SFL == 0 || !C::kHalves, "linear scales");
+      const int r = tn * 8 + (lane & 7);
+      vb[tn][0] = vb[tn][1] = r < rows_b ? (uint32_t)(r * ld + 16 * (lane >> 3)) : 0x80000000u;
+      vbs[tn] = r < rows_b ? (uint32_t)((r + (lane & 8 ? p.N / 2 : 0)) * lds + sw) : 0x80000000u;
+      continue;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = (tn % C::kBlkN) * 16 + 8 * h + (lane & 7);

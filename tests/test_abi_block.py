@@ -79,8 +79,12 @@ def test_gated_refusals():
     assert _gatedq(q=FAKE + 4) == ALIGN and _gatedq(gs=FAKE + 2) == ALIGN
     need = nv.nvfp4_gemm_gated_workspace_size(16, 2048, 6144)
     assert need > 0
-    assert _gated(I=2048, K=6144) == WORKSPACE
-    assert _gated(I=2048, K=6144, ws=FAKE, wsb=need - 1) == WORKSPACE
+    assert _gatedq(I=2048, K=6144) == WORKSPACE
+    assert _gatedq(I=2048, K=6144, ws=FAKE, wsb=need - 1) == WORKSPACE
+    need = nv.nvfp4_gemm_gated_workspace_size(256, 2048, 6144)
+    assert need > 0
+    assert _gated(M=256, I=2048, K=6144) == WORKSPACE
+    assert _gated(M=256, I=2048, K=6144, ws=FAKE, wsb=need - 1) == WORKSPACE
 
 
 def test_ffn_refusals():
@@ -123,7 +127,7 @@ def test_queries():
     # one split, its counters, or partials of S tiles behind 4096 bytes of counters
     assert nv.nvfp4_gemm_epilogue_workspace_size(333, 2001, 1536) == 0
     assert nv.nvfp4_gemm_epilogue_workspace_size(1024, 768, 6144) == 4096 + 192 * 4 * 64 * 64 * 4
-    assert nv.nvfp4_gemm_gated_plan(1, 2048, 6144).startswith("gatedreg16x16")
+    assert nv.nvfp4_gemm_gated_plan(1, 2048, 6144).startswith("gatedreg16x8")
     assert nv.nvfp4_gemm_gated_plan(8192, 8192, 6144).startswith("gated256x128")
     for f in (nv.nvfp4_gemm_epilogue_plan, nv.nvfp4_gemm_gated_plan):
         assert f(16, 16, 100) == "none" and f(0, 16, 256) == "none" and f(1 << 22, 1 << 22, 256) == "none" and f(1 << 30, 32, 256) == "none"

@@ -63,7 +63,7 @@ def test_activations(act):
 
 
 @pytest.mark.parametrize("kind,splits", [(9, 0), (9, 3), (10, 0), (10, 2), (12, 0), (12, 3), (14, 0), (15, 0), (15, 4),
-                                         (16, 0), (32, 0), (32, 2)])
+                                         (16, 0), (32, 0), (32, 2), (33, 0), (33, 3)])
 @pytest.mark.parametrize("M,I,K", [(70, 272, 1536), (257, 99, 768)])
 def test_every_plan_forced(kind, splits, M, I, K, force_plan):
     force_plan(nv.FAMILY_GEMM, kind, splits)
