@@ -428,7 +428,7 @@ const char* nvfp4_mx_gemm_plan(int64_t M, int64_t N, int64_t K);
  * shared f16 A tile, 32-row and 64-row register kernels; the packed and fused
  * calls take kind 3 as 64-row passes and anything else as 32-row passes).
  * family 0 also steers the GEMMs with a fused epilogue below, where they have
- * the kind: 9..12, 14..16 and 32 (16 x 32 register tiles); gated 9, 10, 12, 14, 15,
+ * the kind: 9..12, 14..16, 32 (16 x 32 register tiles) and 34 (9 with 8 waves); gated 9, 10, 12, 14, 15,
  * 32 and, to bf16, 33 (16 x 8).  kind < 0 restores the library's choice.  The plan and workspace queries
  * follow the override.  Not synchronised with calls in flight on other
  * threads: set it while no call of the family is being made.  ERR_SHAPE for

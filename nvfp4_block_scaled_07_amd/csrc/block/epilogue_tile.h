@@ -190,7 +190,7 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
     EpilogueLaunch p) {
   typedef Staging<C> St;
   static_assert(C::MF == 32, "32 x 32 blocks");
-  static_assert(St::kByWave || C::kGroupWaves == 1, "K-group tiles hold one wave's columns in order");
+  static_assert(St::kByWave || !C::kGated || C::kGroupWaves == 1, "gated K-group tiles hold one wave's columns in order");
   __shared__ __attribute__((aligned(16))) SharedEpilogue<C> shm;
   __shared__ int last_flag;
   const TileAt at = tile_at(p.g);
@@ -239,11 +239,12 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
     const bool lead = wave_id() < C::kGroupWaves;  // K-group 0 holds the sum
     if (S == 1) {
       if (lead) {
+        float* dst = shm.stage + wave_id() / C::WN * C::kWM * St::kTileLd + wave_id() % C::WN * C::kWN;
 #pragma unroll
         for (int tm = 0; tm < C::TM; ++tm)
 #pragma unroll
           for (int tn = 0; tn < C::TN; ++tn)
-            stage_block<C, St::kTileLd>(shm.stage + tm * 32 * St::kTileLd + tn * 32, acc[tm][tn]);
+            stage_block<C, St::kTileLd>(dst + tm * 32 * St::kTileLd + tn * 32, acc[tm][tn]);
       }
     } else {
       // publish this split's partial, count arrivals, the last one reduces

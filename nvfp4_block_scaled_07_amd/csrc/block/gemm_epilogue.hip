@@ -16,6 +16,12 @@
 namespace nvfp4 {
 
 typedef Cfg<64, 64, 1, 1, 32, 256, 2, 0, 4, 4> EpiTile64k4;
+// the same tile with two waves a K-group, each half of the columns, for calls
+// whose work-groups have a CU each: two waves per SIMD hide each other's LDS
+// reads (333 x 2001 x 1536: 9.0 us against 9.8; 256 x 768 x 6144 in five splits 10.9
+// against 11.9); with two work-groups per CU the doubled dequantisation of A
+// costs more (1024 x 2048 x 6144: 33.7 against 31.4)
+typedef Cfg<64, 64, 1, 2, 32, 256, 2, 0, 4, 4> EpiTile64k4w8;
 typedef Cfg<128, 128, 2, 2, 32, 256, 2, 0, 1, 2> EpiTile128;
 typedef Cfg<64, 64, 1, 1, 32, 256, 2, 0, 4, 4, 16, 0, 0, 1> GatedTile64k4;  // 32 gate and 32 up columns
 typedef Cfg<128, 128, 2, 2, 32, 256, 2, 0, 1, 2, 16, 0, 0, 1> GatedTile128;
@@ -162,13 +168,14 @@ static void launch_kreg_epilogue(const EpilogueLaunch& p, unsigned grid, hipStre
 
 // Plan kinds, numbered like the plain GEMM's kinds of the same tile; bn is the
 // output columns of a tile (a gated tile's B has twice as many).
-static constexpr int kReg16x32 = 32, kReg16x8 = 33;  // tiles that only the block GEMMs have
+static constexpr int kReg16x32 = 32, kReg16x8 = 33, kTile64w8 = 34;  // tiles that only the block GEMMs have
 struct BlockKind {
   int kind;
   PlanKind k;
 };
 static const BlockKind kEpiKinds[] = {
     {9, {"tile64x64k4", 64, 64, 256, true, false, false, 4}},
+    {kTile64w8, {"tile64x64k4w8", 64, 64, 256, true, false, false, 4}},
     {10, {"kreg16x16k8", 16, 16, 256, true, true, false, EpiReg16x16::KS, EpiReg16x16::D}},
     {11, {"kreg32x16k8", 32, 16, 256, true, true, false, EpiReg32x16::KS, EpiReg32x16::D}},
     {12, {"kreg32x32k8", 32, 32, 256, true, true, false, EpiReg32x32::KS, EpiReg32x32::D}},
@@ -291,7 +298,12 @@ GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K) {
     if (pl.kind >= 14) return pl;
     kind = 9;
   }
-  return plan_of(*find_kind(kEpiKinds, kind), kind, M, N, K, fs, false);
+  GemmPlan pl = plan_of(*find_kind(kEpiKinds, kind), kind, M, N, K, fs, false);
+  if (pl.kind == 9 && fk != 9 && pl.tiles_m * pl.tiles_n * pl.splits <= kCUs) {
+    pl.kind = kTile64w8;
+    pl.name = find_kind(kEpiKinds, kTile64w8)->name;
+  }
+  return pl;
 }
 
 // halves: 16 x 8 tiles, 8 gate and 8 up rows in one block of columns, have enough
@@ -333,6 +345,7 @@ hipError_t launch_gemm_epilogue(const GemmPlan& pl, EpilogueLaunch p, hipStream_
     case 14:
     case 16: launch_epilogue_large(pl.kind, p, grid, stream); break;
     case 15: launch_epilogue_tile<EpiTile128, false>(p, grid, stream); break;
+    case kTile64w8: launch_epilogue_tile<EpiTile64k4w8, false>(p, grid, stream); break;
     default: launch_epilogue_tile<EpiTile64k4, false>(p, grid, stream); break;
   }
   return hipGetLastError();

@@ -57,7 +57,7 @@ def test_activations_bias_and_residual(act, bias, residual):
 
 
 @pytest.mark.parametrize("kind,splits", [(9, 0), (9, 3), (10, 0), (10, 2), (11, 0), (11, 2), (12, 0), (12, 3), (14, 0),
-                                         (15, 0), (15, 4), (16, 0), (3, 2), (32, 0), (32, 3), (33, 0)])
+                                         (15, 0), (15, 4), (16, 0), (3, 2), (32, 0), (32, 3), (33, 0), (34, 0), (34, 1), (34, 3)])
 @pytest.mark.parametrize("M,N,K", [(70, 270, 1536), (257, 195, 768)])
 def test_every_plan_forced(kind, splits, M, N, K, force_plan):
     force_plan(nv.FAMILY_GEMM, kind, splits)
