@@ -41,7 +41,7 @@ def _check(M, N, K, seed, act=nv.ACT_NONE, bias=False, residual=False, beta=1.0,
 
 # one shape per plan family, each odd in M or N where the family allows
 SHAPES = [(1, 768, 512), (1, 6144, 2048), (16, 9000, 512), (16, 768, 6144), (5, 33, 256), (31, 4096, 512), (64, 2048, 1024), (128, 4096, 512),
-          (61, 777, 1280), (200, 300, 768), (513, 1025, 512)]
+          (61, 777, 1280), (200, 300, 768), (513, 1025, 512), (1, 1, 256), (17, 2, 768), (65, 7, 256), (300, 1, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -244,3 +244,11 @@ def test_two_calls_at_once_on_two_streams():
     torch.cuda.synchronize()
     for d, w in zip(got, want):
         assert torch.equal(d, w)
+
+
+@pytest.mark.parametrize("M,N,kind", [(3, 40, -1), (70, 72, 9), (70, 72, 34), (40, 40, 14)])
+def test_long_k(M, N, kind, force_plan):
+    # 2^20 terms a sum; operand rows of 512 KB
+    if kind >= 0:
+        force_plan(nv.FAMILY_GEMM, kind, 0)
+    _check(M, N, 1 << 20, 5, act=nv.ACT_NONE, bias=True, residual=True)

@@ -51,7 +51,8 @@ def _check(M, I, K, seed, act=nv.ACT_SILU, bias=False, label=""):
 
 @pytest.mark.parametrize("M,I,K", [(1, 2048, 512), (1, 16, 256), (1, 4112, 256), (16, 9008, 512), (16, 2048, 6144), (5, 33, 256), (31, 4096, 512),
                                    (64, 2048, 1024), (128, 4096, 512), (100, 784, 1280), (333, 1001, 1536),
-                                   (513, 1040, 512)])
+                                   (513, 1040, 512), (1, 1, 256), (17, 3, 512), (70, 9, 256), (9, 2001, 2304), (3, 24, 1 << 20),
+                                   (70, 40, 1 << 20)])
 @pytest.mark.parametrize("bias", [False, True])
 def test_shapes(M, I, K, bias):
     _check(M, I, K, 11 * M + I, bias=bias)
