@@ -176,6 +176,9 @@ struct BlockKind {
 static const BlockKind kEpiKinds[] = {
     {9, {"tile64x64k4", 64, 64, 256, true, false, false, 4}},
     {kTile64w8, {"tile64x64k4w8", 64, 64, 256, true, false, false, 4}},
+    {14, {"tile256x256w8k256_mfma32", 256, 256, 256, false, false, false}},
+    {15, {"tile128x128k256_mfma32", 128, 128, 256, false, false, false}},
+    {16, {"tile256x192w8k256_mfma32", 256, 192, 256, false, false, false}},
     {10, {"kreg16x16k8", 16, 16, 256, true, true, false, EpiReg16x16::KS, EpiReg16x16::D}},
     {11, {"kreg32x16k8", 32, 16, 256, true, true, false, EpiReg32x16::KS, EpiReg32x16::D}},
     {12, {"kreg32x32k8", 32, 32, 256, true, true, false, EpiReg32x32::KS, EpiReg32x32::D}},
@@ -283,52 +286,60 @@ static int register_kind(const BlockKind (&kinds)[N], int64_t M, int64_t cols, i
   return -1;
 }
 
-// Register tiles, else the plain GEMM's plan (the epilogue adds no operand
-// traffic to the main loop) with the splits above.
-GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K) {
+// The LDS tile of the least estimated time.  Rounds of the unsplit tiles at K =
+// 6144, measured: 163 us for 256 work-groups of 256 x 256 (one per CU), 127 for
+// 256 of 256 x 192, 97 for 512 of 128 x 128 (two per CU); the 64-row tiles run
+// four to a CU, and their last round costs what it holds: 10 us and 48 per 1024.
+// The ratios are those of other K too (4096 x 4096 x 6144: 169, 236, 199, 200 us, x
+// 1024: 43, 58, 45, 50; 1024 x 8192 x 6144: 142, 115, 103, 106; 2048 x 6144 x 2048:
+// 63, 53, 61, 64).  Gated tiles do the same
+// work (their columns are half of it).
+template <int N>
+static int tile_kind(const BlockKind (&kinds)[N], int64_t M, int64_t cols) {
+  struct Round {
+    int kind, work_groups;
+    double us;
+  };
+  int best = 9;
+  double least = 10.0 + 48.0 / 1024 * (double)tiles_of(*find_kind(kinds, 9), M, cols);
+  for (const Round& r : {Round{14, kCUs, 163.0}, Round{16, kCUs, 127.0}, Round{15, 2 * kCUs, 97.0}}) {
+    const PlanKind* k = find_kind(kinds, r.kind);
+    if (!k) continue;
+    const double us = r.us * (double)((tiles_of(*k, M, cols) + r.work_groups - 1) / r.work_groups);
+    if (us < least) {
+      best = r.kind;
+      least = us;
+    }
+  }
+  return best;
+}
+
+template <int N>
+static GemmPlan choose_block_plan(const BlockKind (&kinds)[N], int64_t M, int64_t cols, int64_t K, bool gated, bool halves) {
   int fk = -1, fs = 0;
   if (!forced_plan(kForceGemm, &fk, &fs)) fk = -1;
-  int kind = register_kind(kEpiKinds, M, N, K, false);
-  if (find_kind(kEpiKinds, fk)) kind = fk;
-  else fs = 0;
-  if (kind < 0 || fk == 14 || fk == 15 || fk == 16) {
-    GemmPlan pl = choose_plan(M, N, K, kAutoKinds);
-    pl.splits = 1;  // the large tiles are not split here
-    pl.workspace = 0;
-    if (pl.kind >= 14) return pl;
-    kind = 9;
-  }
-  GemmPlan pl = plan_of(*find_kind(kEpiKinds, kind), kind, M, N, K, fs, false);
-  if (pl.kind == 9 && fk != 9 && pl.tiles_m * pl.tiles_n * pl.splits <= kCUs) {
+  const bool forced = find_kind(kinds, fk) && (fk != kReg16x8 || halves);
+  int kind = forced ? fk : register_kind(kinds, M, cols, K, halves);
+  if (kind < 0) kind = tile_kind(kinds, M, cols);
+  return plan_of(*find_kind(kinds, kind), kind, M, cols, K, forced ? fs : 0, gated);
+}
+
+GemmPlan choose_epilogue_plan(int64_t M, int64_t N, int64_t K) {
+  GemmPlan pl = choose_block_plan(kEpiKinds, M, N, K, false, false);
+  int fk = -1, fs = 0;
+  if (pl.kind == 9 && !(forced_plan(kForceGemm, &fk, &fs) && fk == 9) && pl.tiles_m * pl.tiles_n * pl.splits <= kCUs) {
     pl.kind = kTile64w8;
     pl.name = find_kind(kEpiKinds, kTile64w8)->name;
   }
   return pl;
 }
 
-// halves: 16 x 8 tiles, 8 gate and 8 up rows in one block of columns, have enough
+// 16 x 8 tiles, 8 gate and 8 up rows in one block of columns, have enough
 // work-groups to leave K whole (one token, 2048 x 6144: 6.7 us against 8.2 on 16 x
 // 16 tiles in two splits); an NVFP4 block has 16 columns, so they are for bf16.
-//
-// Gated plans, from sweeps of M = 1..4096, I = 768..16384, K = 1024..16384.
-// 256-row tiles (one work-group per CU) where their last round is at least 85%
-// full in the mean (2048 x 4096 x 6144, one full round: 163 us against 191 on
-// 128-row tiles; 1024 x 4096, half a round: 133 against 100), 128-row tiles from
-// one round of two work-groups per CU on (1024 x 4096 x 6144: 100 us against 108.5
-// on 64-row tiles; half a round: 59 against 57), else 64-row tiles.
 GemmPlan choose_gated_plan(int64_t M, int64_t I, int64_t K, bool quantize) {
   const bool halves = !quantize && I * (K / 16) < (int64_t(1) << 30);
-  const int64_t t14 = tiles_of(*find_kind(kGatedKinds, 14), M, I), rounds14 = (t14 + kCUs - 1) / kCUs;
-  int kind = register_kind(kGatedKinds, M, I, K, halves);
-  if (kind < 0) {
-    kind = 9;
-    if (M > 64 && t14 * 100 >= rounds14 * kCUs * 85) kind = 14;
-    else if (M > 64 && tiles_of(*find_kind(kGatedKinds, 15), M, I) >= 2 * kCUs) kind = 15;
-  }
-  int fk = -1, fs = 0;
-  if (forced_plan(kForceGemm, &fk, &fs) && find_kind(kGatedKinds, fk) && (fk != kReg16x8 || halves)) kind = fk;
-  else fs = 0;
-  return plan_of(*find_kind(kGatedKinds, kind), kind, M, I, K, fs, true);
+  return choose_block_plan(kGatedKinds, M, I, K, true, halves);
 }
 
 hipError_t launch_gemm_epilogue(const GemmPlan& pl, EpilogueLaunch p, hipStream_t stream) {

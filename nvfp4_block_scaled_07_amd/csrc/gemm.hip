@@ -974,7 +974,7 @@ void plan_splits(GemmPlan& pl, const PlanKind& k, int64_t K, int forced) {
 // three times, then 128x128 tiles,
 // and tiles of 8 waves, 256x256 or 256x192, once either fills the CUs twice
 // (all staging 256 K per stage: whole 128-byte lines per row).
-GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, uint32_t kinds) {
+GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
   GemmPlan pl;
   int kind = -1;
   int forced_splits = 0;
@@ -1020,7 +1020,7 @@ GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, uint32_t kinds) {
   }
   // a plan forced by nvfp4_force_plan (tuning sweeps and tests only)
   int fk = -1, fs = 0;
-  if (forced_plan(kForceGemm, &fk, &fs) && fk < kNumKinds && (kinds >> fk & 1)) {
+  if (forced_plan(kForceGemm, &fk, &fs) && fk < kNumKinds) {
     kind = fk;
     forced_splits = fs;
   }

@@ -78,10 +78,7 @@ struct PlanKind {
 // tile counts are set.
 void plan_splits(GemmPlan& pl, const PlanKind& k, int64_t K, int forced);
 
-// kinds: bit k set if the caller has plan kind k (a forced plan outside the
-// set is ignored; the library's own choice is always one of kAutoKinds).
-constexpr uint32_t kAutoKinds = 1u << 9 | 1u << 10 | 1u << 11 | 1u << 12 | 1u << 14 | 1u << 15 | 1u << 16;
-GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, uint32_t kinds = ~0u);
+GemmPlan choose_plan(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm(const GemmPlan& plan, GemmLaunch p, hipStream_t stream);
 // Whether an NVFP4 plan reads scales in tiled layout sf_layout in place: the
 // register tiles read both layouts, the automatic LDS tiles the 8 x 4 one;

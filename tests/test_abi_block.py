@@ -117,12 +117,13 @@ def test_norm_refusals():
 
 
 def test_queries():
-    for M, N, K in [(8192, 6144, 6144), (2048, 6144, 16384), (4096, 4096, 6144)]:
+    for M, N, K in [(8192, 6144, 6144), (2048, 6144, 16384), (4096, 8192, 2048)]:
         assert nv.nvfp4_gemm_epilogue_plan(M, N, K) == nv.nvfp4_gemm_plan(M, N, K)
         assert nv.nvfp4_gemm_epilogue_workspace_size(M, N, K) == nv.nvfp4_gemm_workspace_size(M, N, K) == 0
     for (M, N, K), plan in {(1, 768, 6144): "kreg16x16k8", (16, 6144, 2048): "kreg16x32k8", (64, 2048, 6144): "kreg32x16k8",
                             (256, 1024, 2048): "kreg32x32k8", (64, 768, 16384): "kreg32x32k8",
-                            (128, 768, 16384): "tile64x64k4w8", (1024, 768, 6144): "tile64x64k4"}.items():
+                            (128, 768, 16384): "tile64x64k4w8", (1024, 768, 6144): "tile64x64k4",
+                            (4096, 4096, 6144): "tile256x256w8k256_mfma32", (1024, 8192, 2048): "tile128x128k256_mfma32"}.items():
         assert nv.nvfp4_gemm_epilogue_plan(M, N, K) == plan, (M, N, K)
     # one split, its counters, or partials of S tiles behind 4096 bytes of counters
     assert nv.nvfp4_gemm_epilogue_workspace_size(333, 2001, 1536) == 0
