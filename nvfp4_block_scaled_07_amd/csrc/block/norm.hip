@@ -49,6 +49,17 @@ struct Columns {
     if (TAIL == kOverlap) return any(i) && e >= shared(i);
     return first(i) + (TAIL == kShort ? e : 0) < H;
   }
+  // f(e, whether element e counts) for the elements of chunk i.  Rows of whole
+  // chunks skip absent ones with one test (8192 x 4096, layer norms before and
+  // after: 50.7 us against 52.3 with a select an element, 4096 x 16384 140 against
+  // 149; where a row ends
+  // inside a chunk the selects are faster, 777 x 1545 6.4 against 6.6)
+  template <class F>
+  __device__ __forceinline__ void each(int i, F&& f) const {
+    if (TAIL == kNone && !any(i)) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f(e, TAIL == kNone || counts(i, e));
+  }
   // chunk i of a row or vector as packed bf16; columns past H are 0
   __device__ __forceinline__ u4_t load(const uint16_t* row, int i) const {
     if (TAIL == kShort && any(i) && first(i) + 8 > H) return load_tail8(row + first(i), H & 7);
@@ -148,19 +159,16 @@ __device__ __forceinline__ Stats row_stats(const float (&v)[V][8], const Columns
   if constexpr (LAYER) {
     double a = 0.0;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a += at.counts(i, e) ? (double)v[i][e] : 0.0;
+    for (int i = 0; i < V; ++i) at.each(i, [&](int e, bool in) { a += in ? (double)v[i][e] : 0.0; });
     s.mean = row_sum<TPR>(a, cell) * p.inv_h;
   }
   double q = 0.0;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double d = at.counts(i, e) ? (LAYER ? (double)v[i][e] - s.mean : (double)v[i][e]) : 0.0;
+    at.each(i, [&](int e, bool in) {
+      const double d = in ? (LAYER ? (double)v[i][e] - s.mean : (double)v[i][e]) : 0.0;
       q = __builtin_fma(d, d, q);
-    }
+    });
   s.rstd = rstd_of(row_sum<TPR>(q, cell) * p.inv_h, p.eps);
   return s;
 }
