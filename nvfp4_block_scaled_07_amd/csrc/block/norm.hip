@@ -50,10 +50,10 @@ struct Columns {
     return first(i) + (TAIL == kShort ? e : 0) < H;
   }
   // f(e, whether element e counts) for the elements of chunk i.  Rows of whole
-  // chunks skip absent ones with one test (8192 x 4096, layer norms before and
-  // after: 50.7 us against 52.3 with a select an element, 4096 x 16384 140 against
-  // 149; where a row ends
-  // inside a chunk the selects are faster, 777 x 1545 6.4 against 6.6)
+  // chunks skip absent ones with one test (layer norms before and after, 8192 x
+  // 4096: 50.7 us against 52.3 with a select an element; 4096 x 16384: 140 against
+  // 149); where a row ends inside a chunk the selects are faster (777 x 1545: 6.3
+  // against 6.6).
   template <class F>
   __device__ __forceinline__ void each(int i, F&& f) const {
     if (TAIL == kNone && !any(i)) return;
