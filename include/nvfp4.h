@@ -495,6 +495,8 @@ const char* nvfp4_gemm_epilogue_plan(int64_t M, int64_t N, int64_t K);
  * nvfp4_gemm_gated_quantize: the same h, not rounded to bf16 but quantised to
  * NVFP4 by the rules of nvfp4_quantize with the device encode scale *gs (NULL
  * = 1): q uint8 [M][I/2] (8-byte aligned), sf uint8 [M][I/16].  I % 16 == 0.
+ * A block of h that holds a NaN gets scale byte 0x7F (NaN) and codes 0, so that
+ * what reads it is NaN too; infinities saturate (scale 448, code 6).
  *
  * M == 0 or I == 0 is a successful no-op.  workspace:
  * nvfp4_gemm_gated_workspace_size(M, I, K) bytes under the rules of
@@ -546,12 +548,13 @@ size_t nvfp4_ffn_workspace_size(int64_t M, int64_t H, int64_t I);
  * Outputs, each NULL if not wanted (one at least is): r bf16 [T][H]; y bf16
  * [T][H]; q uint8 [T][H/2] (8-byte aligned) with sf uint8 [T][H/16], the
  * NVFP4 quantisation of y (not of its bf16 rounding) by the rules of
- * nvfp4_quantize with the device encode scale *gs (NULL = 1), H % 16 == 0.  r
- * may be x or residual (same pointer and stride); outputs must not otherwise
- * overlap inputs or each other.  ldx, ldres, ldr, ldy: row strides of x,
- * residual, r and y.  y is computed from the unrounded r.  Sums over a row and
- * rstd are fp64, rounded once to fp32; the other steps fp32.  Any H from 1
- * to 2^30; T == 0 is a successful no-op.  No workspace.
+ * nvfp4_quantize with the device encode scale *gs (NULL = 1), H % 16 == 0 (NaN
+ * and infinities as in nvfp4_gemm_gated_quantize).  r may be x or residual
+ * (same pointer and stride); outputs must not otherwise overlap inputs or each
+ * other.  ldx, ldres, ldr, ldy: row strides of x, residual, r and y.  y is
+ * computed from the unrounded r.  Sums over a row and rstd are fp64, rounded
+ * once to fp32; the other steps fp32.  Any H from 1 to 2^30; T == 0 is a
+ * successful no-op.  No workspace.
  */
 typedef enum { NVFP4_NORM_RMS = 0, NVFP4_NORM_LAYER = 1 } nvfp4_norm_kind;
 nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t* post_weight,

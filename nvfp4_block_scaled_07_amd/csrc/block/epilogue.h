@@ -16,6 +16,7 @@
 
 #include "../kreg_tile.h"
 #include "block.h"
+#include "quantize_block.h"
 #include "vec8.h"
 
 namespace nvfp4 {
@@ -132,7 +133,7 @@ __device__ __forceinline__ void finish(const EpilogueLaunch& p, float a0, float 
 #pragma unroll
     for (int i = 0; i < W; ++i) x[i / 4][i % 4] = v[i];
     uint32_t w[2];
-    const uint32_t code = quantize_block16(x, p.gs ? *p.gs : 1.0f, w);
+    const uint32_t code = quantize_lane16(x, p.gs ? *p.gs : 1.0f, w);
     *(u2_t*)(p.q + row * (p.cols / 2) + col / 2) = u2_t{w[0], w[1]};
     p.sf[row * (p.cols / 16) + col / 16] = (uint8_t)code;
   } else {
@@ -183,34 +184,6 @@ __device__ __forceinline__ Scalars load_scalars(const EpilogueLaunch& p, float a
     if (valid && p.res) c.res = at(p.res, row * p.ldr + col);
   }
   return c;
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
-}
-// within a quad: lane ^ 1, lane ^ 2; within a row of 16: mirrors of 8 and 16
-constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
-
-// NVFP4 of a 16-element block held by the 16 lanes of a DPP row, one element
-// each: the quantiser's steps (quantize_block16), the block amax by four DPP
-// maxima.  Every lane of the row must be active.  Returns the scale code;
-// codes: those of the lane's 8 elements (its half of the row).
-__device__ __forceinline__ uint32_t quantize_row16(float x, float gs, uint32_t& codes) {
-  float a = fabsf(x);
-  a = fmaxf(a, __uint_as_float(dpp<kDppXor1>(__float_as_uint(a))));
-  a = fmaxf(a, __uint_as_float(dpp<kDppXor2>(__float_as_uint(a))));
-  a = fmaxf(a, __uint_as_float(dpp<kDppHalfMirror>(__float_as_uint(a))));
-  a = fmaxf(a, __uint_as_float(dpp<kDppMirror>(__float_as_uint(a))));
-  const uint32_t code = e4m3_encode_pos((a / 6.0f) * gs);
-  const float sv = e4m3_value_pos(code);
-  const float v = x * (sv == 0.0f ? 0.0f : gs / sv);
-  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v, v, 1.0f, 0) & 15u;
-  w <<= 4 * (threadIdx.x & 7);
-  w |= dpp<kDppXor1>(w);
-  w |= dpp<kDppXor2>(w);
-  codes = w | dpp<kDppHalfMirror>(w);
-  return code;
 }
 
 // Epilogue of a tile whose sums lie in LDS, row-major with stride LD (gated:

@@ -20,6 +20,7 @@
 // the same steps gives the same bits, the NVFP4 codes and scales among them.
 // The fp64 sums cost two instructions an element, far below the memory time.
 #include "block.h"
+#include "quantize_block.h"
 #include "vec8.h"
 
 namespace nvfp4 {
@@ -183,7 +184,7 @@ __device__ __forceinline__ void store_y(const NormLaunch& p, const Columns<TPR, 
     if (p.q && c < at.H) {
       // H % 16 == 0: the lanes of a pair hold the two halves of a block
       uint32_t codes;
-      const uint32_t sf = quantize_half_block16(f4_t{y[0], y[1], y[2], y[3]}, f4_t{y[4], y[5], y[6], y[7]}, gs, codes);
+      const uint32_t sf = quantize_pair16(f4_t{y[0], y[1], y[2], y[3]}, f4_t{y[4], y[5], y[6], y[7]}, gs, codes);
       *(uint32_t*)(p.q + t * (p.H / 2) + c / 2) = codes;
       if (c % 16 == 0) p.sf[t * (p.H / 16) + c / 16] = (uint8_t)sf;
     }
