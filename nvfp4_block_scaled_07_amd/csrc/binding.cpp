@@ -53,6 +53,16 @@ int64_t prod(int64_t a, int64_t b) {
   return a > INT64_MAX / b ? INT64_MAX : a * b;
 }
 
+// Other Python threads run while one exists: a launch may wait for room in the
+// GPU's queue, and what it waits for may need the interpreter (a host function
+// on the stream).
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // One call being marshalled.  The first thing found wrong is raised as a
 // Python exception and `failed` set; later steps then do nothing.
 struct Call {
@@ -176,7 +186,8 @@ struct Call {
     return contiguous(*t, 0, "workspace");
   }
 
-  // call(stream) on the tensors' GPU; None or the raised exception.
+  // call(stream) on the tensors' GPU, without the interpreter lock (the
+  // caller's arguments keep the tensors alive); None or the raised exception.
   template <class F>
   PyObject* run(int stream_arg, F&& call) {
     if (failed) return nullptr;
@@ -188,11 +199,14 @@ struct Call {
     if (args[stream_arg] == Py_None && device >= 0)
       stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
     int status;
-    if (device >= 0 && device != c10::hip::current_device()) {
-      const c10::DeviceGuard guard(on);
-      status = call(stream);
-    } else {
-      status = call(stream);
+    {
+      const Unlocked unlocked;
+      if (device >= 0 && device != c10::hip::current_device()) {
+        const c10::DeviceGuard guard(on);
+        status = call(stream);
+      } else {
+        status = call(stream);
+      }
     }
     if (status != 0) {
       refuse(status, g_last_error());
