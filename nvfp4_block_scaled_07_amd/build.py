@@ -8,7 +8,8 @@ large-M NVFP4 tiles) is compiled to an object of its own, with the iterative
 ILP instruction scheduler, and so is each source of the block operators
 (``csrc/block``), all at the same time as the rest; one last hipcc call links
 them.  ``csrc/binding.cpp``, the native marshalling of the block operators'
-Python calls, is host code against torch's headers and becomes ``_binding.so``.
+Python calls, is host code against torch's headers and becomes ``_binding.so``;
+the library does not depend on it.
 """
 from __future__ import annotations
 
@@ -79,7 +80,10 @@ def binding_command(out: str = BINDING) -> list:
 def _run(cmd: list, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{cmd[0]} cannot be run: {e}") from e
     # the host pass warns about the device-only target feature; that is harmless
     msgs = [l for l in (res.stdout + res.stderr).splitlines()
             if l.strip() and "packed-fp32-ops" not in l and "is not a recognized feature" not in l]
@@ -89,17 +93,41 @@ def _run(cmd: list, verbose: bool) -> None:
         print("\n".join(msgs))
 
 
+def _remove(path: str) -> None:
+    if os.path.exists(path):
+        os.remove(path)
+
+
 def build(verbose: bool = False) -> str:
     """Compile every HIP source into the in-tree library, and the marshalling
-    module; returns the library's path."""
+    module; returns the library's path.
+
+    The library needs neither torch nor a host compiler: it is in place whatever
+    becomes of the module, which is left out (with a note) without torch, and
+    whose own failure is raised afterwards.  A module of an earlier build never
+    stays beside a newer library."""
     tmp, btmp = LIB + ".tmp", BINDING + ".tmp"
-    with tempfile.TemporaryDirectory(prefix="nvfp4_build_") as objdir:
-        with ThreadPoolExecutor(len(os.sched_getaffinity(0))) as pool:
-            for done in [pool.submit(_run, cmd, verbose) for cmd in [*object_commands(objdir), binding_command(btmp)]]:
+    try:
+        module = binding_command(btmp)
+    except ImportError as e:
+        module = None
+        print(f"{os.path.basename(BINDING)} is left out, the Python calls of the block operators need it: {e}", file=sys.stderr)
+    try:
+        with tempfile.TemporaryDirectory(prefix="nvfp4_build_") as objdir:
+            with ThreadPoolExecutor(len(os.sched_getaffinity(0))) as pool:
+                objects = [pool.submit(_run, cmd, verbose) for cmd in object_commands(objdir)]
+                binding = pool.submit(_run, module, verbose) if module else None
+            for done in objects:
                 done.result()
-        _run(command(tmp, objdir), verbose)
-    os.replace(tmp, LIB)
-    os.replace(btmp, BINDING)
+            _run(command(tmp, objdir), verbose)
+        _remove(BINDING)
+        os.replace(tmp, LIB)
+        if binding:
+            binding.result()
+            os.replace(btmp, BINDING)
+    finally:
+        _remove(tmp)
+        _remove(btmp)
     return LIB
 
 
