@@ -3,7 +3,7 @@
 Argument marshalling only: every function passes device pointers, sizes and
 the current HIP stream to the C ABI of ``libnvfp4_gfx950.so`` (built in-tree by
 ``nvfp4_block_scaled_07_amd.build``); the block operators' calls are marshalled
-by a native module (``_binding.so``, built with it), the others by ctypes.  All arithmetic runs in the library's
+by a native module (``_binding``, built with it), the others by ctypes.  All arithmetic runs in the library's
 HIP kernels; there is no CPU or PyTorch fallback, and a missing library is an
 error.
 
@@ -15,6 +15,7 @@ Tensors are used only as device memory; the stream is
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -529,14 +530,21 @@ _bind = None
 
 def _native():
     """The native marshalling module of the block operators (csrc/binding.cpp),
-    bound to the loaded library; raises if it has not been built."""
+    bound to the loaded library; raises if it has not been built, does not
+    load or was built for another torch."""
     global _bind
     if _bind is None:
-        import torch  # noqa: F401  (the module's tensor types)
+        import torch
+        hint = "run `python -m nvfp4_block_scaled_07_amd.build`"
         try:
-            from . import _binding
+            _binding = importlib.import_module(f"{__name__}._binding")
+        except ModuleNotFoundError as e:
+            raise ImportError(f"{PKG}/_binding is missing: {hint}") from e
         except ImportError as e:
-            raise ImportError(f"{PKG}/_binding.so is missing: run `python -m nvfp4_block_scaled_07_amd.build`") from e
+            raise ImportError(f"{PKG}/_binding does not load ({e}): {hint}") from e
+        built = getattr(_binding, "torch_version", "an unknown one")
+        if built != torch.__version__:
+            raise ImportError(f"{PKG}/_binding was built for torch {built}, this is {torch.__version__}: {hint}")
         names = ("nvfp4_last_error", "nvfp4_gemm_epilogue", "nvfp4_gemm_gated", "nvfp4_gemm_gated_quantize", "nvfp4_ffn",
                  "nvfp4_residual_norm")
         _binding.setup(Nvfp4Error, *[ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names])

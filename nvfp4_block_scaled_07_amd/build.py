@@ -8,14 +8,15 @@ large-M NVFP4 tiles) is compiled to an object of its own, with the iterative
 ILP instruction scheduler, and so is each source of the block operators
 (``csrc/block``), all at the same time as the rest; one last hipcc call links
 them.  ``csrc/binding.cpp``, the native marshalling of the block operators'
-Python calls, is host code against torch's headers and becomes ``_binding.so``;
-the library does not depend on it.
+Python calls, is host code against torch's headers and becomes ``_binding``
+(with the interpreter's suffix); the library does not depend on it.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -23,7 +24,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libnvfp4_gfx950.so")
-BINDING = os.path.join(PKG, "_binding.so")
+# named for the interpreter it is compiled for, so that another one does not load it
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.hip", "gemm.hip", "layout.hip", "moe.hip", "quantize.hip"]
 # sources compiled separately, with extra flags
 SCHED_SOURCES = {"gemm_large.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]}
@@ -65,13 +67,11 @@ def command(out: str = LIB, objdir: str = "") -> list:
 
 def binding_command(out: str = BINDING) -> list:
     """The g++ call that compiles the marshalling module against torch's headers."""
-    import sysconfig
-
     import torch
     t = os.path.dirname(os.path.abspath(torch.__file__))
     rocm = os.path.dirname(os.path.dirname(HIPCC))
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-            "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f'-DNVFP4_TORCH_VERSION="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-isystem", os.path.join(t, "include"), "-isystem", os.path.join(rocm, "include"),
             "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", out,
             "-L", os.path.join(t, "lib"), "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]

@@ -370,4 +370,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", "Argument marshalling 
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject* PyInit__binding() { return PyModule_Create(&kModule); }
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__binding() {
+  PyObject* m = PyModule_Create(&kModule);
+  // the torch whose headers this was compiled against: another one may lay its tensors out differently
+  if (m && PyModule_AddStringConstant(m, "torch_version", NVFP4_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

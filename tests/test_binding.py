@@ -53,3 +53,36 @@ def test_other_threads_run_during_a_call(tmp_path):
     with pytest.raises(nv.Nvfp4Error) as e:
         nv.nvfp4_residual_norm(None, None, None, None, 0, None, 1.0, None, None, 1e-6, 0, None, None, None, None, None, 0, 0)
     assert e.value.status == 2 and "H = 0" in str(e.value)
+
+
+def _native_error(monkeypatch, package_dir):
+    """The ImportError of loading the module from package_dir."""
+    import sys
+    monkeypatch.setattr(nv, "_bind", None)
+    monkeypatch.setattr(nv, "__path__", [str(package_dir)])
+    monkeypatch.delattr(nv, "_binding", raising=False)
+    monkeypatch.delitem(sys.modules, "nvfp4_block_scaled_07_amd._binding", raising=False)
+    with pytest.raises(ImportError) as e:
+        nv._native()
+    return str(e.value)
+
+
+def test_a_missing_module_and_one_that_does_not_load_are_told_apart(tmp_path, monkeypatch):
+    text = _native_error(monkeypatch, tmp_path)
+    assert "is missing" in text and "nvfp4_block_scaled_07_amd.build" in text
+    (tmp_path / "_binding.so").write_bytes(b"not a shared object")
+    text = _native_error(monkeypatch, tmp_path)
+    assert "is missing" not in text and "nvfp4_block_scaled_07_amd.build" in text
+    assert "invalid ELF header" in text or "too short" in text  # the loader's own words
+
+
+def test_a_module_built_for_another_torch_is_refused(monkeypatch):
+    import os
+
+    import torch
+    here = os.path.dirname(nv.__file__)
+    monkeypatch.setattr(torch, "__version__", "1.0.0+other")
+    text = _native_error(monkeypatch, here)
+    assert "1.0.0+other" in text and "nvfp4_block_scaled_07_amd.build" in text
+    monkeypatch.undo()
+    assert nv._native() is not None
