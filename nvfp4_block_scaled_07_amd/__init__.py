@@ -189,11 +189,14 @@ def nvfp4_gemm_workspace_size(M: int, N: int, K: int) -> int:
 
 
 def nvfp4_workspace_init(workspace, stream=None):
-    """Zero-fill a workspace tensor (needed once before its first use)."""
+    """Zero-fill a workspace tensor (needed once before its first use), on the
+    GPU that holds it and that GPU's current stream."""
     if workspace is None:
         return None
-    st = lib().nvfp4_workspace_init(_ptr(workspace, 0, "workspace", "nvfp4_workspace_init"), _bytes(workspace),
-                                    _stream(stream))
+    import torch
+    p = _ptr(workspace, 0, "workspace", "nvfp4_workspace_init")
+    with torch.cuda.device(workspace.device):
+        st = lib().nvfp4_workspace_init(p, _bytes(workspace), _stream(stream))
     _check(st, "nvfp4_workspace_init")
     return workspace
 
