@@ -1,6 +1,6 @@
 // Internal interfaces of the block operators: the GEMMs with a fused epilogue
 // (gemm_epilogue.hip, gemm_epilogue_large.hip) and the norms around a block
-// (norm.hip), between their kernels and their C entry points (api.hip).
+// (norm.hip), between their kernels and their C entry points (block_api.hip).
 #pragma once
 #include "../internal.h"
 

@@ -35,9 +35,10 @@ __device__ __forceinline__ float over_one_plus_exp2(float x, float e) {
 
 // x Phi(x) = max(x, 0) - |x| / 2 erfc(|x| / sqrt 2), which has no cancellation
 // for x < 0.  With z = |x| / sqrt 2 and t = 1 / (1 + z / 2), erfc(z) = t exp2(p(t)
-// - z^2 log2 e); p is a degree-8 Chebyshev fit of log2(erfc(z) exp(z^2) / t)
-// over |x| <= 20 (relative error 6.5 u; erfc is 0 in fp32 beyond).  13 VALU
-// instructions and the two transcendental ones.
+// - z^2 log2 e), the form of Press, Teukolsky, Vetterling and Flannery, Numerical
+// Recipes, section 6.2, with a fit of its own: p is a degree-8 Chebyshev fit of
+// log2(erfc(z) exp(z^2) / t) over |x| <= 20 (relative error 6.5 u; erfc is 0 in
+// fp32 beyond).  About 18 VALU instructions and the two transcendental ones.
 __device__ __forceinline__ float gelu_erf(float x) {
   const float a = fminf(fabsf(x), 20.0f);
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.35355339f, 1.0f));

@@ -268,10 +268,18 @@ static GemmPlan plan_of(const PlanKind& k, int kind, int64_t M, int64_t cols, in
 // that it is split over that many, or gets a larger tile: 64 x 768 x 16384, 14.9
 // us on 16 x 16 tiles, 12.9 on 32 x 32; 128 x 768 x 16384 21.6 on 32 x 16, 16.5 on the
 // 64-row tiles), per 20 for the largest where the 64-row tiles have full rows
-// (256 x 768 x 6144 13.3 us against 11.8); up to M = 16 16 x 16 tiles are split less, and 16 x 32 tiles take
-// over to four work-groups per CU (16 x 16384 x 6144: 16.6 us; 64-row tiles 21).
-// -1: none of them; their one wave per 16 or 32 columns then dequantises A too
-// often.
+// (256 x 768 x 6144 13.3 us against 11.8); up to M = 16 16 x 16 tiles are split
+// less, and 16 x 32 tiles take over to four work-groups per CU (16 x 16384 x 6144:
+// 16.6 us; 64-row tiles 21).  -1: none of them; their one wave per 16 or 32
+// columns then dequantises A too often.
+//
+// The count of K holds for the 16 x 8 tiles too, which is not where the two
+// cross: cold, gated calls of 2048 columns on 16 x 8 and on 16 x 16 tiles take 7.5
+// and 8.6 us at K = 6144 (M = 1; 16 rows 8.2 and 9.3), 7.9 and 9.0 at 6400, 8.2 and
+// 9.2 at 7168, 8.7 and 9.1 at 8192 (16 rows 9.5 and 10.2), the same within noise at
+// 12288 (11 to 12), 14.5 and 13.3 at 16384, and the rule gives them 16 x 16 tiles
+// from 6400 on; 768 and 1024 columns, where it does so above 12288, cross about
+// there.
 template <int N>
 static int register_kind(const BlockKind (&kinds)[N], int64_t M, int64_t cols, int64_t K, bool halves) {
   const int64_t units = K / 256;

@@ -18,7 +18,10 @@
 // rounding per step in the formulas' order (r is not rounded to bf16 before
 // the second norm).  Built without fp contraction, so a plain evaluation of
 // the same steps gives the same bits, the NVFP4 codes and scales among them.
-// The fp64 sums cost two instructions an element, far below the memory time.
+// The fp64 sums cost an RMS norm two instructions an element (a conversion and
+// a fused multiply-add), far below the memory time; a layer norm also adds for
+// its mean and subtracts it before the square and again, with a conversion, in
+// its output, which a call of a few hundred rows waits for as well.
 #include "block.h"
 #include "quantize_block.h"
 #include "vec8.h"
@@ -262,7 +265,11 @@ __global__ __launch_bounds__(TPR * kRowsPerGroup<TPR>) void k_residual_norm(Norm
 
 // Rows too long for the registers: the same steps with the row read again for
 // each sum, one work-group per row.  A thread stores only columns it reads,
-// after its last read of them, so r may be x or res here too.
+// after its last read of them, so r may be x or res here too.  A residual and an
+// RMS norm read both inputs twice, mostly from cache the second time (1000 x
+// 20480: 40 us, 4.1 TB/s of the four arrays; 1000 x 32768 65 us); with layer norms
+// before and after, x is read five times and the residual three (74 and 111 us).
+// The widest rows that registers hold, 1000 x 16384: 27 and 38 us.
 template <int TAIL, bool LAYER>
 __global__ __launch_bounds__(1024) void k_residual_norm_long(NormLaunch p) {
   constexpr int TPR = 1024;
