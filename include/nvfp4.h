@@ -564,6 +564,147 @@ nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t*
                                  uint16_t* y, int64_t ldy, const float* gs, uint8_t* q, uint8_t* sf, int64_t T,
                                  int64_t H, void* stream);
 
+/*
+ * A mixture-of-experts layer on MXFP4 operands, from router logits to its
+ * output: the steps in front of the expert FFN above (routing and row order,
+ * which nvfp4_moe_ffn takes as inputs) and the experts in the MXFP4 format of
+ * nvfp4_mx_gemm.  The pages run the experts with 256 experts and 8 active per
+ * token ("When a Benchmark Crashes: The Elusive FP4 GEMM Comparison on
+ * Blackwell SM120", section "Why This Message Was Written"); they do not
+ * describe these steps.  All calls are asynchronous on stream.
+ *
+ * nvfp4_moe_route: the experts and weights of T tokens from logits x [T][E]
+ * (logits_type, row stride ldl elements, 0 = E):
+ *   s_e = exp(x_e) / sum exp(x)  (NVFP4_SCORE_SOFTMAX)  or  1 / (1 + exp(-x_e))  (NVFP4_SCORE_SIGMOID)
+ *   v_e = s_e + bias[e]          (bias fp32 [E] or NULL: only the choice sees it)
+ *   group value = sum of the group_top (1 or 2) largest v of a group (n_group
+ *   groups of E / n_group consecutive experts); the topk_group largest stay
+ *   ids[t][0..] = the top_k largest v of the groups that stayed, largest first
+ *   weights[t][j] = s of ids[t][j], over their sum if renormalize, times scale
+ * Ties go to the lowest index.  The choice is that of the formulas in 64 bits
+ * (values that fp32 cannot tell apart are compared in fp64); weights are fp32.
+ * A value that is NaN ranks as -infinity, so that top_k experts always come
+ * out; a NaN or +infinity logit makes the softmax weights of its token NaN, a
+ * token whose logits are all -infinity gets weights 0, and weights whose sum
+ * is 0 stay 0.  n_group 1: no groups.  1 <= E <= 1024, 1 <= top_k <= 64 and
+ * top_k <= topk_group E / n_group (E at n_group 1), n_group <= 64 divides E.
+ * logits aligned to their type, bias, ids and weights 4-byte.  T == 0 is a
+ * successful no-op.  Errors: ERR_SHAPE, ERR_UNSUPPORTED above the limits.
+ */
+typedef enum { NVFP4_LOGITS_F32 = 0, NVFP4_LOGITS_BF16 = 1 } nvfp4_logits_type;
+typedef enum { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 } nvfp4_score;
+nvfp4_status nvfp4_moe_route(const void* logits, int32_t logits_type, int64_t ldl, const float* bias, int32_t score,
+                             int32_t n_group, int32_t topk_group, int32_t group_top, int32_t top_k,
+                             int32_t renormalize, float scale, int32_t* ids, float* weights, int64_t T, int32_t E,
+                             void* stream);
+
+/*
+ * nvfp4_moe_sort: the row order that the grouped products and both FFNs take,
+ * from ids int32 [T][top_k] (as nvfp4_moe_route writes them, or any others):
+ * a stable sort by expert.  Output expert e is id first + e, 0 <= e < E (first
+ * = 0: all experts; a GPU that holds a range of them passes its first), ids
+ * outside that range are left out:
+ *   offsets int32 [E + 1]: offsets[e] = number of ids of experts below e
+ *   row_token int32 [T top_k]: the token of each row (rows at or beyond
+ *       offsets[E] are not written)
+ *   token_rows int32 [T][top_k]: the row of each of a token's experts, -1 for
+ *       an id left out (nvfp4_moe_combine and the FFNs add nothing for it)
+ * 1 <= E <= 65535, T top_k <= 2^30, all pointers 4-byte aligned.  A token may
+ * name an expert more than once.  workspace: nvfp4_moe_sort_workspace_size
+ * bytes (may be NULL when that is 0), 256-byte aligned, of any content; calls
+ * that may overlap need workspaces of their own.  T == 0 or top_k == 0: offsets
+ * are written as zeros.
+ */
+nvfp4_status nvfp4_moe_sort(const int32_t* ids, int32_t first, int32_t* offsets, int32_t* row_token,
+                            int32_t* token_rows, int64_t T, int32_t E, int32_t top_k, void* workspace,
+                            size_t workspace_bytes, void* stream);
+size_t nvfp4_moe_sort_workspace_size(int64_t T, int32_t E, int32_t top_k);
+
+/*
+ * MXFP4 quantisation (the operands of nvfp4_mx_gemm): per block of 32
+ * consecutive elements of a row, with p its largest magnitude,
+ *   e = floor(log2 p) - 2            (NVFP4_MX_FLOOR: OCP Microscaling v1.0; magnitudes above 6 2^e saturate)
+ *   e = the least with p <= 6 2^e    (NVFP4_MX_CEIL: nothing saturates)
+ * limited to -127 .. 125, scale byte e + 127 and codes e2m1_rne_saturating(x
+ * 2^-e) (sign kept, so -0 -> 0x8; a block of zeros has scale byte 0).  A block
+ * that holds a NaN gets scale byte 0xFF (NaN) and codes 0; infinities saturate.
+ *
+ * nvfp4_mx_quantize: x fp32 [R][K] -> q uint8 [R][K/2], sf uint8 [R][K/32].
+ * nvfp4_mx_quantize_rows_bf16: bf16 rows x[row_token[i]] of x [T][K] (x[i] if
+ * row_token is NULL, then rows <= T) -> row i of q uint8 [rows][K/2] and sf
+ * uint8 [rows][K/32]; tokens outside [0, T) give zero rows.
+ * K % 32 == 0 (ERR_SHAPE), K <= 2^30; x and q 16-byte aligned, row_token 4-byte.
+ */
+typedef enum { NVFP4_MX_FLOOR = 0, NVFP4_MX_CEIL = 1 } nvfp4_mx_rule;
+nvfp4_status nvfp4_mx_quantize(const float* x, int64_t R, int64_t K, int32_t rule, uint8_t* q, uint8_t* sf,
+                               void* stream);
+nvfp4_status nvfp4_mx_quantize_rows_bf16(const uint16_t* x, const int32_t* row_token, int32_t rule, uint8_t* q,
+                                         uint8_t* sf, int64_t rows, int64_t T, int64_t K, void* stream);
+
+/*
+ * Grouped products of MXFP4 operands.  Row r, offsets[e] <= r < offsets[e +
+ * 1], of the result belongs to expert e; its A row is row row_token[r] of a
+ * (row r if row_token is NULL, then rows <= T), so that a token's activations
+ * are quantised and stored once however many experts it has.  Tokens outside
+ * [0, T) read as zero rows.
+ *
+ * nvfp4_mx_grouped_gemm:
+ *   D[r][n] = bf16_rne( alpha[e] * sum_k xA[row(r)][k] * xB_e[n][k] + bias[e][n] )
+ *   a uint8 [T][K/2], a_sf uint8 [T][K/32]; b uint8 [E][N][K/2], b_sf uint8
+ *   [E][N][K/32]; alpha fp32 [E] or NULL (1); bias bf16 [E][N] or NULL; d bf16
+ *   [rows][N].
+ * nvfp4_mx_grouped_gated_quantize: both projections of a gated feed-forward,
+ *   h = act(alpha[2e] * sum xA xG + bias[e][i]) * (alpha[2e + 1] * sum xA xU + bias[e][I + i])
+ *   not rounded but quantised to MXFP4 with `rule`: q uint8 [rows][I/2], sf
+ *   uint8 [rows][I/32].  b uint8 [E][2I][K/2] (per expert I gate rows, then I up
+ *   rows), b_sf [E][2I][K/32]; alpha fp32 [2E] or NULL; bias bf16 [E][2I] or
+ *   NULL; act: nvfp4_activation.  I % 32 == 0 (ERR_SHAPE).
+ *
+ * offsets: device int32 [E + 1], non-decreasing, within [0, rows]; rows that no
+ * expert covers are not written, experts without rows read no weights.
+ * status: optional device int32, 0, or 1 + (first bad expert: offsets decrease
+ * or leave [0, rows]; such an expert is skipped), else -(1 + r) for the first
+ * covered row r whose token is outside [0, T).  The scale byte 0xFF is NaN and makes
+ * what reads it NaN.  K % 256 == 0 and K <= 2^22 as for nvfp4_mx_gemm; T K < 2^32,
+ * rows and N <= 2^30, E <= 65535 and E ceil(N / 64) < 2^24 (ERR_UNSUPPORTED).
+ * a, a_sf, b, b_sf 16-byte aligned, d and bias 2-byte, q 2-byte, the others 4-byte.
+ * No workspace.  rows, N (I) or E == 0: nothing but status is written.
+ */
+nvfp4_status nvfp4_mx_grouped_gemm(const uint8_t* a, const uint8_t* a_sf, const int32_t* row_token, const uint8_t* b,
+                                   const uint8_t* b_sf, const int32_t* offsets, const float* alpha,
+                                   const uint16_t* bias, uint16_t* d, int64_t rows, int64_t T, int64_t N, int64_t K,
+                                   int32_t E, int32_t* status, void* stream);
+nvfp4_status nvfp4_mx_grouped_gated_quantize(const uint8_t* a, const uint8_t* a_sf, const int32_t* row_token,
+                                             const uint8_t* b, const uint8_t* b_sf, const int32_t* offsets,
+                                             const float* alpha, const uint16_t* bias, int32_t act, int32_t rule,
+                                             uint8_t* q, uint8_t* sf, int64_t rows, int64_t T, int64_t I, int64_t K,
+                                             int32_t E, int32_t* status, void* stream);
+
+/*
+ * nvfp4_mx_moe_ffn: the experts of one layer, the MXFP4 counterpart of
+ * nvfp4_moe_ffn on the rows of nvfp4_moe_sort:
+ *   xq   = nvfp4_mx_quantize_rows_bf16(x, NULL, rule)                         [T][H]
+ *   h    = nvfp4_mx_grouped_gated_quantize(xq, row_token, w_gu, act, rule)    [T top_k][I]
+ *   down = nvfp4_mx_grouped_gemm(h, w_d)                                      [T top_k][H] bf16
+ *   out  = nvfp4_moe_combine(down, token_rows, token_weight)                  [T][H] bf16
+ * x bf16 [T][H]; w_gu uint8 [E][2I][H/2], w_d uint8 [E][H][I/2] with their
+ * scales; alpha_gu fp32 [2E], bias_gu bf16 [E][2I], alpha_d fp32 [E], bias_d
+ * bf16 [E][H], each NULL if not wanted; token_rows int32, token_weight fp32
+ * [T][top_k] (a row outside the rows covered by offsets adds unspecified values
+ * unless it is negative, which adds nothing).  H % 256 == 0 and I % 256 == 0.
+ * workspace: nvfp4_mx_moe_ffn_workspace_size bytes, 256-byte aligned, of any
+ * content; calls that may overlap (two captured graphs among them) need
+ * workspaces of their own.  status as above.  T == 0 is a successful no-op.
+ */
+nvfp4_status nvfp4_mx_moe_ffn(const uint16_t* x, const int32_t* row_token, const int32_t* offsets,
+                              const uint8_t* w_gu, const uint8_t* w_gu_sf, const float* alpha_gu,
+                              const uint16_t* bias_gu, int32_t act, int32_t rule, const uint8_t* w_d,
+                              const uint8_t* w_d_sf, const float* alpha_d, const uint16_t* bias_d,
+                              const int32_t* token_rows, const float* token_weight, uint16_t* out, int64_t T,
+                              int64_t H, int64_t I, int32_t E, int32_t top_k, void* workspace,
+                              size_t workspace_bytes, int32_t* status, void* stream);
+size_t nvfp4_mx_moe_ffn_workspace_size(int64_t T, int64_t H, int64_t I, int32_t top_k);
+
 /* Message describing the calling thread's last error ("" if none). */
 const char* nvfp4_last_error(void);
 

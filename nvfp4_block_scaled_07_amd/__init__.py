@@ -2,8 +2,8 @@
 
 Argument marshalling only: every function passes device pointers, sizes and
 the current HIP stream to the C ABI of ``libnvfp4_gfx950.so`` (built in-tree by
-``nvfp4_block_scaled_07_amd.build``); the block operators' calls are marshalled
-by a native module (``_binding``, built with it), the others by ctypes.  All arithmetic runs in the library's
+``nvfp4_block_scaled_07_amd.build``); the calls of the block operators and of the
+mixture-of-experts operators on MXFP4 operands are marshalled by a native module (``_binding``, built with it), the others by ctypes.  All arithmetic runs in the library's
 HIP kernels; there is no CPU or PyTorch fallback, and a missing library is an
 error.
 
@@ -82,6 +82,19 @@ SIGNATURES = {
     "nvfp4_ffn_workspace_size": (_sz, [_i64, _i64, _i64]),
     "nvfp4_residual_norm": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _f32, _i32, _vp,
                                            _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp]),
+    "nvfp4_moe_route": (ctypes.c_int, [_vp, _i32, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _i64,
+                                       _i32, _vp]),
+    "nvfp4_moe_sort": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _sz, _vp]),
+    "nvfp4_moe_sort_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "nvfp4_mx_quantize": (ctypes.c_int, [_vp, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "nvfp4_mx_quantize_rows_bf16": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _i64, _i64, _i64, _vp]),
+    "nvfp4_mx_grouped_gemm": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i32,
+                                             _vp, _vp]),
+    "nvfp4_mx_grouped_gated_quantize": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp,
+                                                       _i64, _i64, _i64, _i64, _i32, _vp, _vp]),
+    "nvfp4_mx_moe_ffn": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _i64, _i64, _i64, _i32, _i32, _vp, _sz, _vp, _vp]),
+    "nvfp4_mx_moe_ffn_workspace_size": (_sz, [_i64, _i64, _i64, _i32]),
 }
 
 # nvfp4_force_plan families
@@ -532,8 +545,8 @@ _bind = None
 
 
 def _native():
-    """The native marshalling module of the block operators (csrc/binding.cpp),
-    bound to the loaded library; raises if it has not been built, does not
+    """The native marshalling module of the block operators and the
+    mixture-of-experts operators (csrc/binding.cpp), bound to the loaded library; raises if it has not been built, does not
     load or was built for another torch."""
     global _bind
     if _bind is None:
@@ -548,9 +561,13 @@ def _native():
         built = getattr(_binding, "torch_version", "an unknown one")
         if built != torch.__version__:
             raise ImportError(f"{PKG}/_binding was built for torch {built}, this is {torch.__version__}: {hint}")
+        address = lambda n: ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value
         names = ("nvfp4_last_error", "nvfp4_gemm_epilogue", "nvfp4_gemm_gated", "nvfp4_gemm_gated_quantize", "nvfp4_ffn",
                  "nvfp4_residual_norm")
-        _binding.setup(Nvfp4Error, *[ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in names])
+        _binding.setup(Nvfp4Error, *map(address, names))
+        names = ("nvfp4_moe_route", "nvfp4_moe_sort", "nvfp4_mx_quantize", "nvfp4_mx_quantize_rows_bf16",
+                 "nvfp4_mx_grouped_gemm", "nvfp4_mx_grouped_gated_quantize", "nvfp4_mx_moe_ffn")
+        _binding.setup_experts(*map(address, names))
         _bind = _binding
     return _bind
 
@@ -643,3 +660,96 @@ def nvfp4_residual_norm(x, post_weight, post_bias, gate, gate_group: int, residu
     (_bind or _native()).residual_norm(x, post_weight, post_bias, gate, gate_group, residual, beta, weight, bias, eps,
                                      kind, r, y, gs, q, sf, T, H, stream)
     return r, y, q, sf
+
+
+# nvfp4_score and nvfp4_mx_rule
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+MX_FLOOR, MX_CEIL = 0, 1
+
+
+def nvfp4_moe_route(logits, bias, score: int, n_group: int, topk_group: int, group_top: int, top_k: int,
+                    renormalize: bool, scale: float, ids, weights, T: int, E: int, stream=None):
+    """The top_k experts of each token and their weights; see include/nvfp4.h.
+    logits: fp32 or bf16 [T][E], any row stride; bias: fp32 [E] or None; score:
+    SCORE_*; n_group 1: no groups; ids: int32 [T][top_k]; weights: fp32
+    [T][top_k].  (ids, weights) is returned."""
+    (_bind or _native()).moe_route(logits, bias, score, n_group, topk_group, group_top, top_k, renormalize, scale, ids,
+                                   weights, T, E, stream)
+    return ids, weights
+
+
+def nvfp4_moe_sort_workspace_size(T: int, E: int, top_k: int) -> int:
+    return int(lib().nvfp4_moe_sort_workspace_size(T, E, top_k))
+
+
+def nvfp4_moe_sort(ids, first: int, offsets, row_token, token_rows, T: int, E: int, top_k: int, workspace=None,
+                   stream=None):
+    """The rows of ids int32 [T][top_k] in the order of experts first .. first +
+    E - 1: offsets int32 [E + 1], row_token int32 [T top_k], token_rows int32
+    [T][top_k]; see include/nvfp4.h.  (offsets, row_token, token_rows) is returned."""
+    (_bind or _native()).moe_sort(ids, first, offsets, row_token, token_rows, T, E, top_k, workspace, stream)
+    return offsets, row_token, token_rows
+
+
+def moe_sort_workspace(T: int, E: int, top_k: int, device="cuda"):
+    """Allocate the workspace nvfp4_moe_sort needs (None if none)."""
+    import torch
+    need = nvfp4_moe_sort_workspace_size(T, E, top_k)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def nvfp4_mx_quantize(x, R: int, K: int, rule: int, q, sf, stream=None):
+    """MXFP4 of fp32 x [R][K]: q uint8 [R][K/2], sf uint8 [R][K/32]; rule: MX_*.
+    (q, sf) is returned."""
+    (_bind or _native()).mx_quantize(x, R, K, rule, q, sf, stream)
+    return q, sf
+
+
+def nvfp4_mx_quantize_rows_bf16(x, row_token, rule: int, q, sf, rows: int, T: int, K: int, stream=None):
+    """MXFP4 of bf16 rows x[row_token[i]] (x[i] when row_token is None).  (q,
+    sf) is returned."""
+    (_bind or _native()).mx_quantize_rows(x, row_token, rule, q, sf, rows, T, K, stream)
+    return q, sf
+
+
+def nvfp4_mx_grouped_gemm(a, a_sf, row_token, b, b_sf, offsets, alpha, bias, d, rows: int, T: int, N: int, K: int,
+                          E: int, status=None, stream=None):
+    """Each expert's rows of MXFP4 a [T][K] (row r is a[row_token[r]], or a[r])
+    with its weights b [E][N][K]: d bf16 [rows][N]; see include/nvfp4.h.  alpha:
+    fp32 [E] or None; bias: bf16 [E][N] or None.  d is returned."""
+    (_bind or _native()).mx_grouped_gemm(a, a_sf, row_token, b, b_sf, offsets, alpha, bias, d, rows, T, N, K, E, status,
+                                         stream)
+    return d
+
+
+def nvfp4_mx_grouped_gated_quantize(a, a_sf, row_token, b, b_sf, offsets, alpha, bias, act: int, rule: int, q, sf,
+                                    rows: int, T: int, I: int, K: int, E: int, status=None, stream=None):
+    """The gate and up projections of each expert's rows by b [E][2I][K], their
+    activation and product, to MXFP4 q uint8 [rows][I/2], sf uint8 [rows][I/32];
+    see include/nvfp4.h.  alpha: fp32 [2E] or None; bias: bf16 [E][2I] or None.
+    (q, sf) is returned."""
+    (_bind or _native()).mx_grouped_gated_quantize(a, a_sf, row_token, b, b_sf, offsets, alpha, bias, act, rule, q, sf,
+                                                   rows, T, I, K, E, status, stream)
+    return q, sf
+
+
+def nvfp4_mx_moe_ffn_workspace_size(T: int, H: int, I: int, top_k: int) -> int:
+    return int(lib().nvfp4_mx_moe_ffn_workspace_size(T, H, I, top_k))
+
+
+def mx_moe_ffn_workspace(T: int, H: int, I: int, top_k: int, device="cuda"):
+    """Allocate the workspace nvfp4_mx_moe_ffn needs (None if none)."""
+    import torch
+    need = nvfp4_mx_moe_ffn_workspace_size(T, H, I, top_k)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def nvfp4_mx_moe_ffn(x, row_token, offsets, w_gu, w_gu_sf, alpha_gu, bias_gu, act: int, rule: int, w_d, w_d_sf,
+                     alpha_d, bias_d, token_rows, token_weight, out, T: int, H: int, I: int, E: int, top_k: int,
+                     workspace, status=None, stream=None):
+    """The experts of one MXFP4 layer for bf16 tokens x [T][H] in the row order
+    of nvfp4_moe_sort: out bf16 [T][H]; see include/nvfp4.h.  out is returned."""
+    (_bind or _native()).mx_moe_ffn(x, row_token, offsets, w_gu, w_gu_sf, alpha_gu, bias_gu, act, rule, w_d, w_d_sf,
+                                    alpha_d, bias_d, token_rows, token_weight, out, T, H, I, E, top_k, workspace,
+                                    status, stream)
+    return out

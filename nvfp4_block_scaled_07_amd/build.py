@@ -6,10 +6,11 @@ contraction is off and fp32 division stays correctly rounded.  Packed fp32
 instructions are disabled for all device code.  ``gemm_large.hip`` (the two
 large-M NVFP4 tiles) is compiled to an object of its own, with the iterative
 ILP instruction scheduler, and so is each source of the block operators
-(``csrc/block``), all at the same time as the rest; one last hipcc call links
-them.  ``csrc/binding.cpp``, the native marshalling of the block operators'
-Python calls, is host code against torch's headers and becomes ``_binding``
-(with the interpreter's suffix); the library does not depend on it.
+(``csrc/block``) and of the mixture-of-experts operators (``csrc/experts``),
+all at the same time as the rest; one last hipcc call links them.
+``csrc/binding.cpp``, the native marshalling of their Python calls, is host
+code against torch's headers and becomes ``_binding`` (with the interpreter's
+suffix); the library does not depend on it.
 """
 from __future__ import annotations
 
@@ -36,6 +37,14 @@ BLOCK_SOURCES = {
     "block/gemm_epilogue.hip": [],
     "block/gemm_epilogue_large.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
 }
+# the mixture-of-experts operators on MXFP4 operands
+EXPERT_SOURCES = {
+    "experts/experts_api.hip": [],
+    "experts/moe_route.hip": [],
+    "experts/moe_sort.hip": [],
+    "experts/mx_quantize.hip": [],
+    "experts/mx_grouped.hip": [],
+}
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -54,14 +63,14 @@ def _object(objdir: str, src: str) -> str:
 def object_commands(objdir: str) -> list:
     """hipcc calls that compile every source to an object in objdir."""
     flags = [f for f in FLAGS if f != "-shared"]
-    sources = {**{s: [] for s in SOURCES}, **SCHED_SOURCES, **BLOCK_SOURCES}
+    sources = {**{s: [] for s in SOURCES}, **SCHED_SOURCES, **BLOCK_SOURCES, **EXPERT_SOURCES}
     return [[HIPCC, *flags, *extra, "-c", os.path.join(CSRC, src), "-o", _object(objdir, src)]
             for src, extra in sources.items()]
 
 
 def command(out: str = LIB, objdir: str = "") -> list:
     """The hipcc call that links the objects in objdir."""
-    objs = [_object(objdir, s) for s in [*SOURCES, *SCHED_SOURCES, *BLOCK_SOURCES]]
+    objs = [_object(objdir, s) for s in [*SOURCES, *SCHED_SOURCES, *BLOCK_SOURCES, *EXPERT_SOURCES]]
     return [HIPCC, *FLAGS, *objs, "-o", out]
 
 

@@ -1,0 +1,149 @@
+"""nvfp4_moe_route against the fp64 oracle: the same experts, weights within the
+fp32 error of the scores."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_07_amd as nv
+from oracle import experts_ref as x
+from tests.gpu_util import host, say
+
+pytestmark = pytest.mark.gpu
+
+# relative error of a weight: a softmax score at most 35 U (two exponentials of 1 ulp with a rounded
+# argument, a sum of 22 additions, a reciprocal), the same of the sum of the chosen, four more roundings
+WEIGHT = 76 * 2.0 ** -24
+
+
+def run(logits, bias, score, groups, top_groups, group_top, k, renorm=True, scale=1.0):
+    T, E = logits.shape
+    ids = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), -7.0, device="cuda")
+    nv.nvfp4_moe_route(logits, bias, score, groups, top_groups, group_top, k, renorm, scale, ids, w, T, E)
+    return host(ids), host(w)
+
+
+def check(logits, bias, score, groups, top_groups, group_top, k, renorm=True, scale=1.0):
+    got, w = run(logits, bias, score, groups, top_groups, group_top, k, renorm, scale)
+    want, ww = x.route(logits.float().cpu().numpy(), None if bias is None else bias.cpu().numpy(), score, groups,
+                       top_groups, group_top, k, renorm, scale)
+    np.testing.assert_array_equal(got, want)
+    assert (np.isnan(w) == np.isnan(ww)).all()
+    assert (np.abs(w - ww) <= WEIGHT * np.abs(ww) + 2.0 ** -140)[~np.isnan(ww)].all(), np.nanmax(np.abs(w / ww - 1))
+    return got, w
+
+
+CONFIGS = [  # T, E, groups, top_groups, group_top, k
+    (1, 1, 1, 1, 1, 1), (5, 2, 1, 1, 1, 2), (3, 8, 1, 1, 1, 2), (37, 60, 1, 1, 1, 4), (9, 60, 4, 2, 2, 6),
+    (64, 64, 1, 1, 1, 8), (65, 65, 5, 3, 2, 8), (130, 128, 8, 3, 1, 6), (33, 160, 8, 3, 1, 6), (257, 256, 8, 4, 2, 8),
+    (7, 257, 1, 1, 1, 9), (18, 384, 1, 1, 1, 8), (6, 512, 64, 5, 2, 40), (4, 1000, 1, 1, 1, 64), (3, 1024, 32, 32, 2, 10),
+    (11, 48, 48, 7, 2, 5), (11, 63, 21, 20, 2, 60),
+]
+
+
+@pytest.mark.parametrize("score", [nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("T,E,groups,top_groups,group_top,k", CONFIGS)
+def test_choice_and_weights(T, E, groups, top_groups, group_top, k, with_bias, score):
+    say("route", T, E, groups, top_groups, group_top, k, with_bias, score)
+    g = torch.Generator(device="cuda").manual_seed(T * 1000 + E)
+    logits = torch.randn(T, E, device="cuda", generator=g) * 1.5
+    bias = torch.randn(E, device="cuda", generator=g) * 0.1 if with_bias else None
+    check(logits, bias, score, groups, top_groups, group_top, k, True, 2.5)
+    check(logits.bfloat16(), bias, score, groups, top_groups, group_top, k, False, 1.0)  # many equal logits
+
+
+def test_values_that_fp32_cannot_tell_apart():
+    # biases that bring every score to about 0.9: what decides is the rounding of the bias itself
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for score, E, groups, kept, top in ((nv.SCORE_SIGMOID, 256, 8, 4, 2), (nv.SCORE_SIGMOID, 100, 1, 1, 1),
+                                        (nv.SCORE_SOFTMAX, 128, 4, 2, 2), (nv.SCORE_SOFTMAX, 600, 1, 1, 1)):
+        row = torch.randn(1, E, device="cuda", generator=g)
+        s = torch.softmax(row.double(), -1) if score == nv.SCORE_SOFTMAX else torch.sigmoid(row.double())
+        bias = (0.9 - s[0]).float()
+        v = s[0] + bias.double()
+        assert v.unique().numel() > E // 2 and float(v.max() - v.min()) < 2e-7
+        check(row.repeat(6, 1), bias, score, groups, kept, top, 8)
+
+
+def test_ties_take_the_lowest_index():
+    logits = torch.zeros(3, 256, device="cuda")
+    logits[1, 100:130] = 1.0
+    logits[2] = torch.arange(256, device="cuda") // 16 % 2
+    for groups, kept, top in ((1, 1, 1), (8, 4, 2), (16, 3, 1)):
+        for bias in (None, torch.zeros(256, device="cuda"), torch.full((256,), 0.25, device="cuda")):
+            for score in (nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID):
+                check(logits, bias, score, groups, kept, top, 8)
+
+
+def test_infinities_and_nan():
+    inf, nan = float("inf"), float("nan")
+    logits = torch.randn(7, 40, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4))
+    logits[0] = -inf
+    logits[1, 5:] = -inf          # fewer finite than top_k
+    logits[2, 3] = nan
+    logits[3, 3] = inf
+    logits[4] = nan
+    logits[5, ::2] = -3.0e38
+    bias = torch.zeros(40, device="cuda")
+    bias[7], bias[8] = -inf, -3e38
+    for b in (None, bias):
+        for score in (nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID):
+            for groups, kept, top in ((1, 1, 1), (4, 2, 2), (4, 3, 1)):
+                for renorm in (True, False):
+                    ids, _ = run(logits, b, score, groups, kept, top, 8, renorm)
+                    want, ww = x.route(logits.cpu().numpy(), None if b is None else b.cpu().numpy(), score, groups, kept,
+                                       top, 8, renorm, 1.0)
+                    assert all(len(set(r)) == 8 and min(r) >= 0 and max(r) < 40 for r in ids.tolist())
+                    finite = [1, 5, 6] if score == nv.SCORE_SOFTMAX else [0, 1, 2, 3, 4, 5, 6]
+                    np.testing.assert_array_equal(ids[finite], want[finite], err_msg=f"{score} {groups} {b is None}")
+                    np.testing.assert_array_equal(ids[0], want[0])
+    w = run(logits, None, nv.SCORE_SOFTMAX, 1, 1, 1, 8)[1]
+    assert (w[0] == 0).all() and np.isnan(w[2]).all() and np.isnan(w[3]).any() and np.isnan(w[4]).all()
+
+
+def test_row_strides_other_stream_and_graph():
+    g = torch.Generator(device="cuda").manual_seed(5)
+    wide = torch.randn(50, 301, device="cuda", generator=g)
+    for t in (wide[:, 3:259], wide.bfloat16()[:, 1:257], wide.bfloat16()[:, 44:300]):
+        check(t, None, nv.SCORE_SOFTMAX, 8, 4, 2, 8)
+    logits = wide[:, :256].contiguous()
+    bias = torch.zeros(256, device="cuda")
+    ids, w = torch.empty(50, 8, dtype=torch.int32, device="cuda"), torch.empty(50, 8, device="cuda")
+    args = (logits, bias, nv.SCORE_SIGMOID, 8, 4, 2, 8, True, 1.0, ids, w, 50, 256)
+    nv.nvfp4_moe_route(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.nvfp4_moe_route(*args)
+    for _ in range(3):
+        logits.copy_(torch.randn(50, 256, device="cuda", generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        got, gw = host(ids).copy(), host(w).copy()
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        ids.zero_()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            nv.nvfp4_moe_route(*args)
+        torch.cuda.current_stream().wait_stream(s)
+        np.testing.assert_array_equal(got, host(ids))
+        np.testing.assert_array_equal(gw, host(w))
+
+
+def test_refused_tensors():
+    logits = torch.randn(4, 8, device="cuda")
+    ids, w = torch.empty(4, 2, dtype=torch.int32, device="cuda"), torch.empty(4, 2, device="cuda")
+
+    def call(**kw):
+        a = dict(logits=logits, bias=None, score=0, n_group=1, topk_group=1, group_top=1, top_k=2, renormalize=True, scale=1.0,
+                 ids=ids, weights=w, T=4, E=8)
+        a.update(kw)
+        return nv.nvfp4_moe_route(**a)
+    call()
+    for bad in (dict(logits=logits.half()), dict(logits=logits.cpu()), dict(logits=logits.t()), dict(T=5), dict(E=9),
+                dict(ids=ids.long()), dict(ids=ids[:, :1]), dict(weights=w.double()), dict(bias=torch.zeros(7, device="cuda")),
+                dict(bias=torch.zeros(8, device="cuda").bfloat16()), dict(top_k=9), dict(logits=None)):
+        with pytest.raises(nv.Nvfp4Error):
+            call(**bad)
