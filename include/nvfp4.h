@@ -662,11 +662,14 @@ nvfp4_status nvfp4_mx_quantize_rows_bf16(const uint16_t* x, const int32_t* row_t
  *
  * offsets: device int32 [E + 1], non-decreasing, within [0, rows]; rows that no
  * expert covers are not written, experts without rows read no weights.
- * status: optional device int32, 0, or 1 + (first bad expert: offsets decrease
- * or leave [0, rows]; such an expert is skipped), else -(1 + r) for the first
- * covered row r whose token is outside [0, T).  The scale byte 0xFF is NaN and makes
+ * status: optional device int32, 0, or 1 + (first bad expert: its offsets
+ * decrease or leave [0, rows]; it is skipped), else -(1 + r) for the first
+ * covered row r whose token is outside [0, T).  Where offsets decrease, rows
+ * that two experts claim, and those of later experts, may be written or left.
+ * The scale byte 0xFF is NaN and makes
  * what reads it NaN.  K % 256 == 0 and K <= 2^22 as for nvfp4_mx_gemm; T K < 2^32,
- * rows and N <= 2^30, E <= 65535 and E ceil(N / 64) < 2^24 (ERR_UNSUPPORTED).
+ * rows and N <= 2^30, E <= 65535 and (rows / 16 + min(E, rows)) ceil(N / 64) <
+ * 2^24 (ERR_UNSUPPORTED).
  * a, a_sf, b, b_sf 16-byte aligned, d and bias 2-byte, q 2-byte, the others 4-byte.
  * No workspace.  rows, N (I) or E == 0: nothing but status is written.
  */

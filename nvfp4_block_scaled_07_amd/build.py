@@ -44,6 +44,7 @@ EXPERT_SOURCES = {
     "experts/moe_sort.hip": [],
     "experts/mx_quantize.hip": [],
     "experts/mx_grouped.hip": [],
+    "experts/mx_grouped_tile.hip": [],
 }
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -68,5 +68,7 @@ struct MxGroupedLaunch {
 hipError_t launch_expert_status(const int32_t* offsets, int E, const int32_t* row_token, int64_t rows, int64_t T,
                                 int32_t* status, hipStream_t stream);
 hipError_t launch_mx_grouped(const MxGroupedLaunch& p, bool gated, hipStream_t stream);
+// ... by the 256 x 256 tiles for experts of many rows (mx_grouped_tile.hip)
+void launch_mx_grouped_tile(const MxGroupedLaunch& p, bool gated, hipStream_t stream);
 
 }  // namespace nvfp4

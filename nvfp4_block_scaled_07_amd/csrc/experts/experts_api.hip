@@ -57,9 +57,9 @@ nvfp4_status check_sizes(const char* fn, int64_t rows, int64_t T, int64_t N, con
   // row offsets of a in 32 bits; a launch has fewer than 2^32 threads
   if (T > ((int64_t(1) << 32) - 1) / K)
     return fail(NVFP4_ERR_UNSUPPORTED, "%s: T = %lld rows of K = %lld: T K < 2^32 is supported", fn, (ll)T, (ll)K);
-  if (E * ((N + 63) / 64) >= (int64_t(1) << 24))
-    return fail(NVFP4_ERR_UNSUPPORTED, "%s: %d experts of %s = %lld: fewer than 2^24 tiles of 64 columns are supported", fn, E,
-                nname, (ll)N);
+  if ((rows / 16 + (rows < E ? rows : E)) * ((N + 63) / 64) >= (int64_t(1) << 24))
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: rows = %lld of %d experts, %s = %lld: fewer than 2^24 tiles of 16 x 64 are supported",
+                fn, (ll)rows, E, nname, (ll)N);
   return NVFP4_OK;
 }
 

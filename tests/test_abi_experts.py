@@ -106,7 +106,7 @@ def test_product_refusals(call):
     assert call(tok=None) == SHAPE and "row_token" in nv.nvfp4_last_error()
     assert call(T=1 << 24) == UNSUPPORTED and "T K" in nv.nvfp4_last_error()
     assert call(T=1 << 62) == UNSUPPORTED and call(rows=1 << 31) == UNSUPPORTED and call(N=1 << 31) == UNSUPPORTED
-    assert call(E=65536) == UNSUPPORTED and call(E=65535, N=1 << 20) == UNSUPPORTED
+    assert call(E=65536) == UNSUPPORTED and call(E=65535, N=1 << 20, rows=1 << 20) == UNSUPPORTED
     for name in ("a", "a_sf", "b", "b_sf"):
         assert call(**{name: None}) == NULL and call(**{name: FAKE + 8}) == ALIGN
     assert call(offsets=None) == NULL
