@@ -583,10 +583,10 @@ nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t*
  *   weights[t][j] = s of ids[t][j], over their sum if renormalize, times scale
  * Ties go to the lowest index.  The choice is that of the formulas in 64 bits
  * (values that fp32 cannot tell apart are compared in fp64); weights are fp32.
- * A value that is NaN ranks as -infinity, so that top_k experts always come
- * out; a NaN or +infinity logit makes the softmax weights of its token NaN, a
- * token whose logits are all -infinity gets weights 0, and weights whose sum
- * is 0 stay 0.  n_group 1: no groups.  1 <= E <= 1024, 1 <= top_k <= 64 and
+ * A value that is NaN ranks below all others, and top_k different experts
+ * always come out.  A NaN or +infinity logit makes softmax weights of its token
+ * NaN, and which experts it gets is then not specified; a token whose logits
+ * are all -infinity gets weights 0, and weights whose sum is 0 stay 0.  n_group 1: no groups.  1 <= E <= 1024, 1 <= top_k <= 64 and
  * top_k <= topk_group E / n_group (E at n_group 1), n_group <= 64 divides E.
  * logits aligned to their type, bias, ids and weights 4-byte.  T == 0 is a
  * successful no-op.  Errors: ERR_SHAPE, ERR_UNSUPPORTED above the limits.

@@ -34,7 +34,7 @@ struct SortLaunch {
   int32_t* token_rows; // [T top_k]
   int64_t n;           // T top_k
   int top_k, E;
-  int32_t* ws;
+  uint16_t* ws;
 };
 size_t moe_sort_workspace(int64_t n, int E);
 hipError_t launch_moe_sort(const SortLaunch& p, hipStream_t stream);

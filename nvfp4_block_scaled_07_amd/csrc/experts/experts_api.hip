@@ -173,7 +173,7 @@ nvfp4_status nvfp4_moe_sort(const int32_t* ids, int32_t first, int32_t* offsets,
   p.n = n;
   p.top_k = top_k;
   p.E = E;
-  p.ws = (int32_t*)workspace;
+  p.ws = (uint16_t*)workspace;
   return hip_status(nvfp4::launch_moe_sort(p, (hipStream_t)stream), fn);
 }
 

@@ -31,9 +31,9 @@ def scores(x: np.ndarray, score: int) -> np.ndarray:
 
 
 def best(v: np.ndarray, n: int) -> np.ndarray:
-    """Indices of the n largest of a vector, largest first, ties to the lowest index."""
-    left = [(-float(x), i) for i, x in enumerate(np.where(np.isnan(v), -np.inf, v))]
-    return np.array([i for _, i in sorted(left)[:n]], np.int64)
+    """Indices of the n largest of a vector, largest first, ties to the lowest index, NaN last."""
+    left = [(bool(np.isnan(x)), 0.0 if np.isnan(x) else -float(x), i) for i, x in enumerate(v)]
+    return np.array([i for _, _, i in sorted(left)[:n]], np.int64)
 
 
 def route(logits, bias, score: int, groups: int, top_groups: int, group_top: int, top_k: int, renormalize: bool, scale):
@@ -42,12 +42,12 @@ def route(logits, bias, score: int, groups: int, top_groups: int, group_top: int
     T, E = x.shape
     s = scores(x, score)
     v = s if bias is None else s + np.asarray(bias, np.float64)
-    v = np.where(np.isnan(v), -np.inf, v)
     size = E // groups
     ids = np.empty((T, top_k), np.int32)
     w = np.empty((T, top_k))
     for t in range(T):
-        sums = np.array([sum(sorted(v[t, g * size:(g + 1) * size])[::-1][:group_top]) for g in range(groups)])
+        parts = v[t].reshape(groups, size)
+        sums = np.array([part[best(part, group_top)].sum() for part in parts])
         kept = sorted(best(sums, top_groups))
         experts = np.concatenate([np.arange(g * size, (g + 1) * size) for g in kept])
         ids[t] = experts[best(v[t, experts], top_k)]

@@ -78,13 +78,15 @@ def test_ties_take_the_lowest_index():
 
 def test_infinities_and_nan():
     inf, nan = float("inf"), float("nan")
-    logits = torch.randn(7, 40, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4))
+    logits = torch.randn(8, 40, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4))
     logits[0] = -inf
     logits[1, 5:] = -inf          # fewer finite than top_k
     logits[2, 3] = nan
     logits[3, 3] = inf
     logits[4] = nan
     logits[5, ::2] = -3.0e38
+    logits[7] = -inf              # no finite one, and NaN
+    logits[7, 2:30:3] = nan
     bias = torch.zeros(40, device="cuda")
     bias[7], bias[8] = -inf, -3e38
     for b in (None, bias):
@@ -95,7 +97,7 @@ def test_infinities_and_nan():
                     want, ww = x.route(logits.cpu().numpy(), None if b is None else b.cpu().numpy(), score, groups, kept,
                                        top, 8, renorm, 1.0)
                     assert all(len(set(r)) == 8 and min(r) >= 0 and max(r) < 40 for r in ids.tolist())
-                    finite = [1, 5, 6] if score == nv.SCORE_SOFTMAX else [0, 1, 2, 3, 4, 5, 6]
+                    finite = [1, 5, 6] if score == nv.SCORE_SOFTMAX else list(range(8))
                     np.testing.assert_array_equal(ids[finite], want[finite], err_msg=f"{score} {groups} {b is None}")
                     np.testing.assert_array_equal(ids[0], want[0])
     w = run(logits, None, nv.SCORE_SOFTMAX, 1, 1, 1, 8)[1]

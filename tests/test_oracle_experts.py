@@ -46,6 +46,8 @@ def test_ties_nan_and_empty_rows():
     assert ids.tolist() == [[0, 1]] and (w == 0).all()
     ids, w = x.route([[np.nan, -inf, 1.0, 0.0]], None, x.SIGMOID, 1, 1, 1, 3, False, 1.0)
     assert ids.tolist() == [[2, 3, 1]] and w[0, 2] == 0
+    ids, w = x.route([[np.nan, -inf, 1.0, 0.0]], None, x.SIGMOID, 1, 1, 1, 4, False, 1.0)
+    assert ids.tolist() == [[2, 3, 1, 0]] and np.isnan(w[0, 3])
 
 
 def test_sort_rows_by_hand():
