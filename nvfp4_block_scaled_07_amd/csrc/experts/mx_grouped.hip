@@ -392,11 +392,11 @@ static void launch_rows(const MxGroupedLaunch& p, hipStream_t stream) {
   // The host knows the average rows of an expert only.  Measured (us, both
   // products of a feed-forward of 2048 x 6144, rows on average, by tile height
   // 16 / 32 / 64 / 256): 2 rows 727 / 734 / 792, 16 rows 1113 / 926 / 973, 64 rows
-  // 729 / 448 / 355 / 395, 96 rows - / - / 443 / 466, 128 rows - / - / 543 / 497
+  // 729 / 448 / 356 / 377, 80 rows 436 / 383 by the last two, 128 rows 543 / 417
   // (256 experts up to 16 rows, 64 from there).
   if (p.rows <= 4 * (int64_t)p.E) launch_stream<16, GATED>(p, stream);
   else if (p.rows <= 24 * (int64_t)p.E) launch_stream<32, GATED>(p, stream);
-  else if (p.rows <= 112 * (int64_t)p.E) launch_stream<64, GATED>(p, stream);
+  else if (p.rows <= 72 * (int64_t)p.E) launch_stream<64, GATED>(p, stream);
   else launch_mx_grouped_tile(p, GATED, stream);
 }
 

@@ -1,8 +1,11 @@
 // Grouped products of MXFP4 operands where experts have many rows: 256 rows x
 // 256 weight rows a work-group, 8 waves of 128 x 64, both operands staged in
-// LDS (the stage ring and MFMA loop of the plain MX GEMM's 256 x 256 tile, in
-// gemm_tile.h).  Bound by the matrix pipes; see mx_grouped.hip for the formulas
-// and for the kernel that serves few rows.
+// LDS.  Bound by the matrix pipes (65536 rows on 32 experts of 2 x 2048 x 6144:
+// 1012 to 1046 us over boxes, 3.2 PFLOP/s; the plain MX GEMM of 8192^3 3.3 to
+// 3.5), and with a short K by the stores of the outputs as well, which all
+// work-groups issue at the same time (32768 rows of 6144 x 2048 on 64 experts: 407
+// us, 325 without them).  See mx_grouped.hip for the formulas and for the kernel
+// that serves few rows.
 //
 // A's rows are gathered on the way into LDS: the lanes of a load instruction
 // that belong to one row add that row's own offset.  The weights are the MFMA's
@@ -30,6 +33,7 @@ struct CfgExperts : Cfg<256, 256, 2, 4, 32, 256, 2, 0, 1, 2, 32, 4> {
   static constexpr int kBWave = GATED ? kWN / 2 : kWN;    // and of one wave in it
   static constexpr int b_row(int tn) { return GATED ? tn * kBRows : tn * MF; }
   static_assert(TN == 2, "gated: one column block of each matrix a wave");
+  static_assert(BM == BN, "both operands' stage buffers are as far apart");
 };
 
 // LDS reads of sub-step SS of stage buffer BUF.
@@ -79,6 +83,11 @@ __device__ __forceinline__ void tile_stage(const ReadAddr<C>& ra, typename C::Ac
         acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bv[tn], av[tm], acc[tm][tn], 4, 4, 0,
                                                                        (int)cur.bsw[tn], 0, (int)cur.asw[tm]);
   });
+  // computed here: not moved down to where the tile ends (no instruction reads it)
+#pragma unroll
+  for (int tm = 0; tm < C::TM; ++tm)
+#pragma unroll
+    for (int tn = 0; tn < C::TN; ++tn) asm volatile("" : "+v"(acc[tm][tn]));
 }
 
 // Row offsets of this lane's pieces of A, in the order of issue_a.
@@ -139,76 +148,76 @@ __device__ __forceinline__ u4_t eight_columns(const float (&v)[8]) {
   return w;
 }
 
-template <class C>
-__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_mx_grouped_tile(MxGroupedLaunch p) {
-  __shared__ __attribute__((aligned(16))) Smem<C> sm;
-  constexpr int kCols = C::kBRows;  // output columns of a tile
-  const int64_t cols = C::kGated ? p.N / 2 : p.N;
-  const int tiles_n = (int)((cols + kCols - 1) / kCols);
-  const int L = xcd_remap(blockIdx.x, gridDim.x);
-  const ExpertTile at = find_tile<C::BM>(p, L / tiles_n);
-  if (at.expert < 0) return;
-  // within an expert row tiles run fastest: they share the weights' tile
-  const int in = L - at.first * tiles_n, e = at.expert;
-  const int64_t n0 = (int64_t)(in / at.tiles) * kCols, mc = at.lo + (int64_t)(in % at.tiles) * C::BM;
-  const int rows_c = (int)min<int64_t>(C::BM, at.hi - mc);
-  const int64_t ld = p.K / 2, lds = p.K / 32;
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  const int wm = wave / C::WN, wn = wave % C::WN;
+// A tile's expert, rows and columns.
+struct TileAtExpert {
+  int e, rows_c, cols_c;  // expert (-1: no such tile), valid rows, valid columns
+  int64_t mc, n0;         // first row, first column
+};
 
-  const int64_t row0 = (int64_t)e * p.N + n0, second = C::kGated ? p.N / 2 : 0;
-  const Operand B{p.b + row0 * ld, p.b_sf + row0 * lds, ld, lds, (int)min<int64_t>(kCols, cols - n0),
-                  p.b + (row0 + second) * ld, p.b_sf + (row0 + second) * lds};
+// One tile, and where its operands are.
+template <class C>
+struct TileJob : TileAtExpert {
+  Operand B;
+  rsrc_t ra, ras;
+  GatherA<C> ga;
+};
+
+// Logical tile L: the column tiles of a row tile are apart by the expert's row
+// tiles, so that neighbours share the weights' tile.
+template <class C>
+__device__ __forceinline__ TileJob<C> tile_job(const MxGroupedLaunch& p, int L, int tiles_n) {
   typedef GatherA<C> G;
-  G ga;
+  TileJob<C> t;
+  const ExpertTile at = find_tile<C::BM>(p, L / tiles_n);
+  t.e = at.expert;
+  if (t.e < 0) return t;
+  const int64_t cols = C::kGated ? p.N / 2 : p.N, ld = p.K / 2, lds = p.K / 32;
+  const int in = L - at.first * tiles_n, lane = threadIdx.x & 63, wave = wave_id();
+  t.n0 = (int64_t)(in / at.tiles) * C::kBRows;
+  t.mc = at.lo + (int64_t)(in % at.tiles) * C::BM;
+  t.rows_c = (int)min<int64_t>(C::BM, at.hi - t.mc);
+  t.cols_c = (int)min<int64_t>(C::kBRows, cols - t.n0);
+  const int64_t row0 = (int64_t)t.e * p.N + t.n0, second = C::kGated ? p.N / 2 : 0;
+  t.B = Operand{p.b + row0 * ld, p.b_sf + row0 * lds, ld, lds, t.cols_c, p.b + (row0 + second) * ld, p.b_sf + (row0 + second) * lds};
   const bool gather = p.row_token != nullptr;
-  const rsrc_t ra = gather ? uniform_rsrc(p.a, (uint32_t)(p.T * ld)) : uniform_rsrc(p.a + mc * ld, (uint32_t)(rows_c * ld));
-  const rsrc_t ras = gather ? uniform_rsrc(p.a_sf, (uint32_t)(p.T * lds)) : uniform_rsrc(p.a_sf + mc * lds, (uint32_t)(rows_c * lds));
+  t.ra = gather ? uniform_rsrc(p.a, (uint32_t)(p.T * ld)) : uniform_rsrc(p.a + t.mc * ld, (uint32_t)(t.rows_c * ld));
+  t.ras = gather ? uniform_rsrc(p.a_sf, (uint32_t)(p.T * lds)) : uniform_rsrc(p.a_sf + t.mc * lds, (uint32_t)(t.rows_c * lds));
   const auto source = [&](int r) -> int64_t {  // row r's row of a, or -1
-    if (r >= rows_c) return -1;
+    if (r >= t.rows_c) return -1;
     if (!gather) return r;
-    const int64_t t = p.row_token[mc + r];
-    return t >= 0 && t < p.T ? t : -1;
+    const int64_t k = p.row_token[t.mc + r];
+    return k >= 0 && k < p.T ? k : -1;
   };
 #pragma unroll
   for (int i = 0; i < G::kCodes; ++i) {
     const int r = (wave % C::kDmaWaves + i * C::kDmaWaves) * G::Codes::kRowsPerInst + lane / C::CH;
-    const int64_t t = source(r);
-    ga.code[i] = t < 0 ? 0x80000000u : (uint32_t)(t * ld + (((lane % C::CH) ^ swz<C::CH, C::MF>(r)) << 4));
+    const int64_t k = source(r);
+    t.ga.code[i] = k < 0 ? 0x80000000u : (uint32_t)(k * ld + (((lane % C::CH) ^ swz<C::CH, C::MF>(r)) << 4));
   }
 #pragma unroll
   for (int i = 0; i < G::kScales; ++i) {
     const int r = (wave % C::kDmaWaves + i * C::kDmaWaves) * G::Scales::kRowsPerInst + lane / (C::SB / 4);
-    const int64_t t = source(r);
-    ga.scale[i] = t < 0 ? 0x80000000u : (uint32_t)(t * lds + (lane % (C::SB / 4)) * 4);
+    const int64_t k = source(r);
+    t.ga.scale[i] = k < 0 ? 0x80000000u : (uint32_t)(k * lds + (lane % (C::SB / 4)) * 4);
   }
+  return t;
+}
 
-  typename C::Acc acc[C::TM][C::TN];
-  zero_acc<C>(acc);
-  const bool works = wm * C::kWM < rows_c;  // this wave has rows (uniform)
-  const int n = (int)(p.K / C::BK);
-  issue_tile<C>(sm, 0, ga, ra, ras, B, 0, wave, lane);
-  wait_vm_barrier<0>();
-  const ReadAddr<C> rd = read_addr<C>(sm);
-  for (int i0 = 0; i0 < n; i0 += 2) {
-    static_for<2>([&](auto jc) {
-      constexpr int J = decltype(jc)::value;
-      const int i = i0 + J;
-      if (i < n) {
-        if (i + 1 < n) issue_tile<C>(sm, 1 - J, ga, ra, ras, B, i + 1, wave, lane);
-        if (works) tile_stage<C, J>(rd, acc);
-        if (i + 1 < n) wait_vm_barrier<0>();
-      }
-    });
-  }
-  if (!works) return;
+// Bytes of an output row in LDS: 64 columns and 16 more (other banks).
+constexpr int kOutRow = 64 * 2 + 16;
 
+template <class C>
+__device__ __forceinline__ void finish_tile(const MxGroupedLaunch& p, const TileAtExpert& t,
+                                            const typename C::Acc (&acc)[C::TM][C::TN], uint8_t* out) {
+  const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN, wn = wave % C::WN;
+  const int e = t.e, rows_c = t.rows_c;
+  const int64_t mc = t.mc, n0 = t.n0;
   // lane: row lane % 32 of each row block; accumulator j is column
   // Mfma<32>::row(j, lane / 32) of each column block
   const int g = lane >> 5;
   if constexpr (C::kGated) {
     const float a0 = p.alpha ? p.alpha[2 * e] : 1.0f, a1 = p.alpha ? p.alpha[2 * e + 1] : 1.0f;
-    const int64_t I = cols, col = n0 + 32 * wn;
+    const int64_t I = p.N / 2, col = n0 + 32 * wn;
     if (col >= I) return;  // blocks of 32 are whole
 #pragma unroll
     for (int tm = 0; tm < C::TM; ++tm) {
@@ -256,36 +265,106 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))
       }
     }
   } else {
+    // through LDS, 16 rows of this wave's 64 columns at a time, so that whole
+    // 128-byte runs of a row are stored (65536 rows of 6144 x 2048 on 32 experts
+    // 691 us against 782 with 32-byte runs from the accumulators)
     const float alpha = p.alpha ? p.alpha[e] : 1.0f;
+    const int col0 = wn * C::kWN;
+    const uint16_t* bias = p.bias ? p.bias + (int64_t)e * p.N + n0 + col0 : nullptr;
+    uint8_t* own = out + wave * 16 * kOutRow;
 #pragma unroll
-    for (int tn = 0; tn < C::TN; ++tn) {
-      const int col = wn * C::kWN + tn * 32;
-      if (col >= B.rows) continue;
-      const uint16_t* bias = p.bias ? p.bias + (int64_t)e * p.N + n0 + col : nullptr;
+    for (int tm = 0; tm < C::TM; ++tm) {
+      u4_t w[C::TN][2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {  // columns 16 c .. 16 c + 15 of the block
-        float b[8];
+      for (int tn = 0; tn < C::TN; ++tn)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int k = Mfma<32>::row(8 * c + j, g);
-          b[j] = bias && col + k < B.rows ? __uint_as_float((uint32_t)bias[k] << 16) : 0.0f;
-        }
-#pragma unroll
-        for (int tm = 0; tm < C::TM; ++tm) {
+        for (int c = 0; c < 2; ++c) {  // columns 16 c .. 16 c + 15 of the block
           float v[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = bias ? alpha * acc[tm][tn][8 * c + j] + b[j] : alpha * acc[tm][tn][8 * c + j];
-          const u4_t w = eight_columns(v);
-          const int row = wm * C::kWM + tm * 32 + (lane & 31), k = col + 16 * c + 8 * g;
-          if (row < rows_c && k < B.rows) {
-            uint16_t* out = p.d + (mc + row) * p.N + n0 + k;
-            if (k + 8 <= B.rows) store8(out, w);
+          for (int j = 0; j < 8; ++j) {
+            const int k = tn * 32 + Mfma<32>::row(8 * c + j, g);
+            v[j] = alpha * acc[tm][tn][8 * c + j];
+            if (bias && col0 + k < t.cols_c) v[j] += __uint_as_float((uint32_t)bias[k] << 16);
+          }
+          w[tn][c] = eight_columns(v);
+        }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if ((lane >> 4 & 1) == half) {
+#pragma unroll
+          for (int tn = 0; tn < C::TN; ++tn)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) *(u4_t*)(own + (lane & 15) * kOutRow + (tn * 32 + 16 * c + 8 * g) * 2) = w[tn][c];
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = 8 * i + (lane >> 3), k = 8 * (lane & 7);
+          const u4_t x = *(const u4_t*)(own + r * kOutRow + 2 * k);
+          const int row = wm * C::kWM + tm * 32 + 16 * half + r, col = col0 + k;
+          if (row < rows_c && col < t.cols_c) {
+            uint16_t* to = p.d + (mc + row) * p.N + n0 + col;
+            if (col + 8 <= t.cols_c) store8(to, x);
             else
-              for (int j = 0; j < B.rows - k; ++j) out[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+              for (int j = 0; j < t.cols_c - col; ++j) to[j] = (uint16_t)(x[j >> 1] >> (16 * (j & 1)));
           }
         }
+        __builtin_amdgcn_wave_barrier();
       }
     }
+  }
+}
+
+// A work-group goes through the tiles that are gridDim.x apart.  The stage ring
+// runs on over the ends of tiles: the next tile is looked up and its first stage
+// loaded under the last products of the one before (8192 rows on 64 experts of
+// 2 x 2048 x 6144 with a work-group a tile 309 us, like this 250; their down
+// projections 187 and 165).
+template <class C>
+__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))) void k_mx_grouped_tile(MxGroupedLaunch p) {
+  __shared__ __attribute__((aligned(16))) Smem<C> sm;
+  __shared__ __attribute__((aligned(16))) uint8_t rows[C::kGated ? 16 : C::kWaves * 16 * kOutRow];
+  const int64_t cols = C::kGated ? p.N / 2 : p.N;
+  const int tiles_n = (int)((cols + C::kBRows - 1) / C::kBRows);
+  const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN;
+  const int n = (int)(p.K / C::BK);
+  int L = xcd_remap(blockIdx.x, gridDim.x);
+  TileJob<C> t = tile_job<C>(p, L, tiles_n);
+  if (t.e < 0) return;
+  issue_tile<C>(sm, 0, t.ga, t.ra, t.ras, t.B, 0, wave, lane);
+  wait_vm_barrier<0>();
+  ReadAddr<C> rd = read_addr<C>(sm);
+  int buf = 0;
+#pragma unroll 1
+  while (true) {
+    typename C::Acc acc[C::TM][C::TN];
+    zero_acc<C>(acc);
+    const bool works = wm * C::kWM < t.rows_c;  // this wave has rows (uniform)
+    const TileAtExpert out = t;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      if (i + 1 < n) {
+        issue_tile<C>(sm, buf ^ 1, t.ga, t.ra, t.ras, t.B, i + 1, wave, lane);
+      } else {
+        L += gridDim.x;
+        t = tile_job<C>(p, L, tiles_n);
+        if (t.e >= 0) issue_tile<C>(sm, buf ^ 1, t.ga, t.ra, t.ras, t.B, 0, wave, lane);
+      }
+      if (works) tile_stage<C, 0>(rd, acc);
+      wait_vm_barrier<0>();
+      // the other buffer
+      const uint32_t step = buf ? 0u - C::BM * C::RB : C::BM * C::RB, sstep = buf ? 0u - C::BM * C::SB : C::BM * C::SB;
+#pragma unroll
+      for (int k = 0; k < ReadAddr<C>::kS; ++k) {
+        rd.a[k] += step;
+        rd.b[k] += step;
+      }
+      rd.as += sstep;
+      rd.bs += sstep;
+      buf ^= 1;
+    }
+    if (works) finish_tile<C>(p, out, acc, rows);
+    if (t.e < 0) return;
   }
 }
 
@@ -293,8 +372,8 @@ template <bool GATED>
 static void launch_tile(const MxGroupedLaunch& p, hipStream_t stream) {
   typedef CfgExperts<GATED> C;
   const int64_t cols = GATED ? p.N / 2 : p.N, kCols = C::kBRows;
-  hipLaunchKernelGGL(k_mx_grouped_tile<C>, dim3((unsigned)(most_tiles(p.rows, p.E, C::BM) * ((cols + kCols - 1) / kCols))),
-                     dim3(C::kThreads), 0, stream, p);
+  const int64_t tiles = most_tiles(p.rows, p.E, C::BM) * ((cols + kCols - 1) / kCols);
+  hipLaunchKernelGGL(k_mx_grouped_tile<C>, dim3((unsigned)(tiles < kCUs ? tiles : kCUs)), dim3(C::kThreads), 0, stream, p);
 }
 
 void launch_mx_grouped_tile(const MxGroupedLaunch& p, bool gated, hipStream_t stream) {
