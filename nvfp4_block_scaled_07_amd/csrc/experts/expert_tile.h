@@ -14,16 +14,20 @@ struct ExpertTile {
 
 // Most row tiles that `rows` rows of E experts have: every expert with rows may
 // have one that is not full.
-inline int64_t most_tiles(int64_t rows, int E, int bm) { return rows / bm + (rows < E ? rows : E); }
+__host__ __device__ inline int64_t most_tiles(int64_t rows, int E, int bm) { return rows / bm + (rows < E ? rows : E); }
 
 // The expert of row tile q, the same in all lanes.  Every wave finds it for
 // itself: lane l counts the tiles of EPL consecutive experts (four at a time,
 // whose offsets are loaded together), a prefix sum over the lanes follows, and
-// the lane that holds q tells.  Experts whose offsets are wrong have no tiles.
+// the lane that holds q tells.  Experts whose offsets are wrong have no tiles.  Offsets
+// that decrease can add up to any number of tiles: q is below most_tiles, which
+// fits kMostTiles (the entry points see to it), and a lane's count stops there.
 // Counting leaves out experts without rows, which are most of them when a few
 // tokens meet many experts (one token, 8 of 256 experts, 2 x 2048 x 6144: 36 us
 // with a work-group for every expert, 22 like this), and spreads an expert of
 // many rows over the GPU.
+constexpr int kMostTiles = 1 << 24;
+
 template <int BM>
 __device__ __forceinline__ ExpertTile find_tile(const MxGroupedLaunch& p, int q) {
   const int lane = threadIdx.x & 63;
@@ -41,7 +45,7 @@ __device__ __forceinline__ ExpertTile find_tile(const MxGroupedLaunch& p, int q)
   int mine = 0;
   for (int e = 0; e < epl; e += 4) {
     load4(e0 + e);
-    mine += n[0] + n[1] + n[2] + n[3];
+    mine = min(mine + min(n[0], kMostTiles) + min(n[1], kMostTiles) + min(n[2], kMostTiles) + min(n[3], kMostTiles), kMostTiles);
   }
   int upto = mine;  // inclusive prefix sum
 #pragma unroll
@@ -59,14 +63,14 @@ __device__ __forceinline__ ExpertTile find_tile(const MxGroupedLaunch& p, int q)
     if (epl > 4) load4(e0 + b);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (e < 0 && q < first + n[i]) {
+      if (e < 0 && q - first < n[i]) {
         e = e0 + b + i;
         lo = at[i];
         hi = at[i + 1];
         tiles = n[i];
         before = first;
       }
-      first += n[i];
+      first += e < 0 ? n[i] : 0;
     }
   }
   t.expert = __builtin_amdgcn_readlane(e, owner);

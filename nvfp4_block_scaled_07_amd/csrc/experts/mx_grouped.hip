@@ -266,25 +266,27 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
 #pragma unroll
     for (int tn = 0; tn < C::TN; ++tn) acc[tm][tn] = Mfma<16>::Acc{0.f, 0.f, 0.f, 0.f};
 
-  // units past the end of K read out of range: zero codes and scales
+  // units past the end of K read out of range: zero codes and scales.  The chunk
+  // behind the last one has no scalar offset, which may lie past a buffer's end.
   const auto stage_load = [&](int c) {
+    const int at = c < chunks ? c : 0;
     const bool piece = C::kU * c + (pc >> 3) < nu, scale = C::kU * c + su < nu;
 #pragma unroll
     for (int i = 0; i < C::kPieces; ++i)
-      st.a[i] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, piece ? va[i] : kOutside, c * C::kRow * 16, 0));
+      st.a[i] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, piece ? va[i] : kOutside, at * C::kRow * 16, 0));
 #pragma unroll
     for (int i = 0; i < C::kASf; ++i)
-      st.as[i] = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(ras, scale ? vas[i] : kOutside, c * C::kU * 8, 0));
+      st.as[i] = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(ras, scale ? vas[i] : kOutside, at * C::kU * 8, 0));
 #pragma unroll
     for (int i = 0; i < C::kBSf; ++i) {
       const uint32_t off = scale ? vbs[i] : kOutside;
       if constexpr (C::kGated) {
         // a thread's rows are of one matrix: it loads from its own
-        const u2_t x = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, odd_block ? kOutside : off, c * C::kU * 8, 0));
-        const u2_t y = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(rs2, odd_block ? off : kOutside, c * C::kU * 8, 0));
+        const u2_t x = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, odd_block ? kOutside : off, at * C::kU * 8, 0));
+        const u2_t y = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(rs2, odd_block ? off : kOutside, at * C::kU * 8, 0));
         st.bs[i] = odd_block ? y : x;
       } else {
-        st.bs[i] = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, off, c * C::kU * 8, 0));
+        st.bs[i] = __builtin_bit_cast(u2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, off, at * C::kU * 8, 0));
       }
     }
   };

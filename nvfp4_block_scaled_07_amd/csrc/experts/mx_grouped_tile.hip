@@ -163,11 +163,14 @@ struct TileJob : TileAtExpert {
 };
 
 // Logical tile L: the column tiles of a row tile are apart by the expert's row
-// tiles, so that neighbours share the weights' tile.
+// tiles, so that neighbours share the weights' tile.  limit: tiles that offsets
+// which do not decrease may have.
 template <class C>
-__device__ __forceinline__ TileJob<C> tile_job(const MxGroupedLaunch& p, int L, int tiles_n) {
+__device__ __forceinline__ TileJob<C> tile_job(const MxGroupedLaunch& p, int L, int tiles_n, int limit) {
   typedef GatherA<C> G;
   TileJob<C> t;
+  t.e = -1;
+  if (L >= limit) return t;
   const ExpertTile at = find_tile<C::BM>(p, L / tiles_n);
   t.e = at.expert;
   if (t.e < 0) return t;
@@ -328,8 +331,9 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))
   const int tiles_n = (int)((cols + C::kBRows - 1) / C::kBRows);
   const int lane = threadIdx.x & 63, wave = wave_id(), wm = wave / C::WN;
   const int n = (int)(p.K / C::BK);
+  const int limit = (int)(most_tiles(p.rows, p.E, C::BM) * tiles_n);
   int L = xcd_remap(blockIdx.x, gridDim.x);
-  TileJob<C> t = tile_job<C>(p, L, tiles_n);
+  TileJob<C> t = tile_job<C>(p, L, tiles_n, limit);
   if (t.e < 0) return;
   issue_tile<C>(sm, 0, t.ga, t.ra, t.ras, t.B, 0, wave, lane);
   wait_vm_barrier<0>();
@@ -347,7 +351,7 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))
         issue_tile<C>(sm, buf ^ 1, t.ga, t.ra, t.ras, t.B, i + 1, wave, lane);
       } else {
         L += gridDim.x;
-        t = tile_job<C>(p, L, tiles_n);
+        t = tile_job<C>(p, L, tiles_n, limit);
         if (t.e >= 0) issue_tile<C>(sm, buf ^ 1, t.ga, t.ra, t.ras, t.B, 0, wave, lane);
       }
       if (works) tile_stage<C, 0>(rd, acc);

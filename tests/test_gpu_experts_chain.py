@@ -109,8 +109,9 @@ def test_experts_of_two_gpus_add_up():
     assert near(a.out, a.want()) <= 5e-3
 
 
-def test_captured_and_replayed():
-    l = Layer(80, 17, 512, 512, 32, 4, 4, 2, True)
+@pytest.mark.parametrize("T,E,k", [(17, 32, 4), (333, 8, 4), (1000, 4, 2)])
+def test_captured_and_replayed(T, E, k):
+    l = Layer(80, T, 512, 512, E, k, 4, 2, True)
     l.run(False)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -118,8 +119,8 @@ def test_captured_and_replayed():
         l.run(False)
     g = torch.Generator(device="cuda").manual_seed(1)
     for _ in range(4):
-        l.t["logits"].copy_(torch.randn(17, 32, device="cuda", generator=g))
-        l.t["x"].copy_(torch.randn(17, 512, device="cuda", generator=g))
+        l.t["logits"].copy_(torch.randn(T, E, device="cuda", generator=g))
+        l.t["x"].copy_(torch.randn(T, 512, device="cuda", generator=g))
         l.out.zero_()
         graph.replay()
         torch.cuda.synchronize()

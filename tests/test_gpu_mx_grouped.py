@@ -98,6 +98,56 @@ def test_gated(name, I, K, gather, rule, act):
         check_mx(host(q), host(sf), h, delta, rule, name)
 
 
+def check_gemm(p, got, bias=None):
+    s, mag = x.expert_products(p["a"], p["a_sf"], p["tok"], p["b"], p["b_sf"], p["off"], p["rows"])
+    bi = 0.0 if bias is None else bias[expert_of(p)].astype(np.float64)
+    assert (np.abs(got.double().cpu().numpy() - (s + bi)) <= product_bound(s, mag, p["K"], 1.0, bi)).all()
+
+
+@pytest.mark.parametrize("K", [256, 768])
+def test_more_tiles_than_work_groups(K):
+    # 8 row tiles of 50 column tiles, the last of each in part: work-groups go through several
+    p = problem(K, [700, 0, 300, 513], 12600, K, True)
+    bias = torch.from_numpy(np.random.default_rng(3).standard_normal((4, 12600)).astype(np.float32) * 50).bfloat16().float().numpy()
+    check_gemm(p, gemm(p, bias=bias), bias)
+    p["a_sf"] = (p["a_sf"].astype(np.int64) - 7).astype(np.uint8)
+    s, mag = x.expert_products(p["a"], p["a_sf"], p["tok"], p["b"], p["b_sf"], p["off"], p["rows"])
+    I = 6272
+    b, b_sf = (np.concatenate([v[:, :I], v[:, -I:]], 1) for v in (p["b"], p["b_sf"]))
+    s, mag = (np.concatenate([v[:, :I], v[:, -I:]], 1) for v in (s, mag))
+    a, a_sf, b, b_sf = dev_mx(p["a"], p["a_sf"], b, b_sf)
+    q, sf = out_bytes(p["rows"], I, 2), out_bytes(p["rows"], I, 32)
+    nv.nvfp4_mx_grouped_gated_quantize(a, a_sf, dev(p["tok"]), b, b_sf, dev(p["off"]), None, None, 0, 1, q, sf, p["rows"], p["T"],
+                                       I, K, 4)
+    (dg, g), (du, u) = (((K + 3) * U * m + 2 * U * np.abs(v), v) for m, v in ((mag[:, :I], s[:, :I]), (mag[:, I:], s[:, I:])))
+    h = g * u
+    check_mx(host(q), host(sf), h, dg * (np.abs(u) + du) + np.abs(g) * du + 4 * U * np.abs(h) + 2.0 ** -140, 1, "persistent")
+
+
+@pytest.mark.parametrize("E,counts", [(300, {0: 3, 3: 1, 255: 17, 256: 2, 299: 40}), (300, {7: 22000, 280: 90}), (1100, {1099: 70, 64: 1}),
+                                      (1100, {1030: 79300})])
+def test_many_experts(E, counts):
+    say("experts", E, counts)
+    n = [counts.get(e, 0) for e in range(E)]
+    check_gemm(*(lambda p: (p, gemm(p)))(problem(E, n, 40, 256, True, T=50)))
+
+
+@pytest.mark.parametrize("rows,N", [(64, 64), (2000, 64), (2000, 300)])
+def test_offsets_that_go_back_and_forth(rows, N):
+    # every other expert claims all rows: it ends, and whole rows come out
+    E = 16
+    p = problem(rows, [rows] + [0] * (E - 1), N, 256, True)
+    p["off"] = np.array([0, rows] * (E // 2) + [0], np.int32)
+    status = torch.full((1,), -9, dtype=torch.int32, device="cuda")
+    p["b"][:], p["b_sf"][:] = p["b"][0], p["b_sf"][0]  # whichever writes a row
+    got = gemm(p, status=status)
+    assert host(status)[0] == 2
+    p["off"] = offsets_of([rows] + [0] * (E - 1))
+    s, mag = x.expert_products(p["a"], p["a_sf"], p["tok"], p["b"], p["b_sf"], p["off"], rows)
+    near = np.abs(got.double().cpu().numpy() - s) <= product_bound(s, mag, 256)
+    assert (near | (host(got.view(torch.int16)) == FILL)).all() and near.any()
+
+
 def test_rows_behind_the_last_expert_stay():
     p = problem(5, [3, 0, 9], 100, 512, True)
     p["tok"] = np.concatenate([p["tok"], np.full(20, 2 ** 30, np.int32)])  # never read
