@@ -36,6 +36,7 @@ struct SortLaunch {
   int top_k, E;
   uint16_t* ws;
 };
+constexpr int kMostSorted = 1024;  // experts of the form for many ids
 size_t moe_sort_workspace(int64_t n, int E);
 hipError_t launch_moe_sort(const SortLaunch& p, hipStream_t stream);
 

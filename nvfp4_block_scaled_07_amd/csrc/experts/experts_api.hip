@@ -157,6 +157,10 @@ nvfp4_status nvfp4_moe_sort(const int32_t* ids, int32_t first, int32_t* offsets,
     return fail(NVFP4_ERR_SHAPE, "%s: T = %lld, top_k = %d, first = %d must be >= 0 and E = %d >= 1", fn, (ll)T, top_k, first, E);
   if (E > 65535 || (top_k > 0 && T > kMaxRows / top_k))
     return fail(NVFP4_ERR_UNSUPPORTED, "%s: E = %d, T = %lld, top_k = %d: E up to 65535 and T top_k up to 2^30", fn, E, (ll)T, top_k);
+  // a work-group an expert goes through all ids
+  if (E > nvfp4::kMostSorted && T * top_k > (1 << 20))
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: T = %lld, top_k = %d: T top_k up to 2^20 above %d experts (E = %d)", fn, (ll)T, top_k,
+                nvfp4::kMostSorted, E);
   const int64_t n = T * top_k;
   if (!offsets || (n > 0 && (!ids || !row_token || !token_rows)))
     return fail(NVFP4_ERR_NULL, "%s: ids, offsets, row_token and token_rows must not be NULL", fn);

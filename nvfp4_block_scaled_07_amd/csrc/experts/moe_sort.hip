@@ -112,7 +112,7 @@ struct SortRuns {
   int runs;
   int64_t per;
 };
-constexpr int kManyRuns = 1024, kMostSorted = 1024;
+constexpr int kManyRuns = 1024;
 constexpr int kAhead = 8;  // steps of 64 ids that a wave loads at once
 static SortRuns sort_runs(int64_t n) {
   SortRuns r;

@@ -71,6 +71,8 @@ def test_route_refusals():
 def test_sort_refusals():
     assert _sort(T=-1) == SHAPE and _sort(E=0) == SHAPE and _sort(top_k=-1) == SHAPE and _sort(first=-1) == SHAPE
     assert _sort(E=65536) == UNSUPPORTED and _sort(T=1 << 30) == UNSUPPORTED and _sort(T=1 << 62) == UNSUPPORTED
+    assert _sort(T=1 << 18, E=1025, top_k=5) == UNSUPPORTED and "1024" in nv.nvfp4_last_error()
+    assert _sort(T=1 << 18, E=1025, top_k=4, ids=None) == NULL
     for name in ("ids", "offsets", "row_token", "token_rows"):
         assert _sort(**{name: None}) == NULL and _sort(**{name: FAKE + 2}) == ALIGN
     assert nv.nvfp4_moe_sort_workspace_size(-1, 8, 2) == 0 and nv.nvfp4_moe_sort_workspace_size(4, 0, 2) == 0

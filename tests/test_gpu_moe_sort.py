@@ -66,6 +66,21 @@ def test_many_rows(T, E, k):
     check(np.full((T, k), E - 1, np.int32), 0, E, fast)  # one expert has all
 
 
+def test_many_experts():
+    # above 1024 experts the form for few ids takes more of them, too
+    ids = np.random.default_rng(5).integers(-2, 1505, (9000, 6)).astype(np.int32)
+    check(ids, 0, 1500, fast)
+    check(ids[:10], 3, 65535, fast)
+
+
+def test_wild_ids_among_many():
+    rng = np.random.default_rng(6)
+    ids = rng.integers(0, 40, (9000, 6)).astype(np.int32)
+    ids.reshape(-1)[::5] = rng.choice([-1, 40, 64, 2 ** 31 - 1, -2 ** 31, -2 ** 31 + 7], ids.reshape(-1)[::5].shape)
+    check(ids, 0, 40, fast)
+    check(ids, 7, 20, fast)
+
+
 def test_no_rows():
     for T, k in ((0, 8), (5, 0)):
         off, tok, _ = run(torch.empty(T, k, dtype=torch.int32, device="cuda"), 0, 6)
