@@ -582,12 +582,16 @@ nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t*
  *   ids[t][0..] = the top_k largest v of the groups that stayed, largest first
  *   weights[t][j] = s of ids[t][j], over their sum if renormalize, times scale
  * Ties go to the lowest index.  The choice is that of the formulas in 64 bits
- * (values that fp32 cannot tell apart are compared in fp64); weights are fp32.
+ * (values that fp32 cannot tell apart are compared in fp64; where scores alone
+ * decide, one by one, their logits are compared, whose order is the scores').
+ * Weights are fp32, within a few units of the last place; scores below 2^-126
+ * may become 0, but for a renormalised weight they count.
  * A value that is NaN ranks below all others, and top_k different experts
  * always come out.  A NaN or +infinity logit makes softmax weights of its token
  * NaN, and which experts it gets is then not specified; a token whose logits
- * are all -infinity gets weights 0, and weights whose sum is 0 stay 0.  n_group 1: no groups.  1 <= E <= 1024, 1 <= top_k <= 64 and
- * top_k <= topk_group E / n_group (E at n_group 1), n_group <= 64 divides E.
+ * are all -infinity gets weights 0, and weights whose sum is 0 in 64 bits stay 0.
+ * n_group 1: no groups.  1 <= E <= 1024, 1 <= top_k <= 64 and top_k <=
+ * topk_group E / n_group (E at n_group 1), n_group <= 64 divides E.
  * logits aligned to their type, bias, ids and weights 4-byte.  T == 0 is a
  * successful no-op.  Errors: ERR_SHAPE, ERR_UNSUPPORTED above the limits.
  */
@@ -609,7 +613,8 @@ nvfp4_status nvfp4_moe_route(const void* logits, int32_t logits_type, int64_t ld
  *       offsets[E] are not written)
  *   token_rows int32 [T][top_k]: the row of each of a token's experts, -1 for
  *       an id left out (nvfp4_moe_combine and the FFNs add nothing for it)
- * 1 <= E <= 65535, T top_k <= 2^30, all pointers 4-byte aligned.  A token may
+ * 1 <= E <= 65535, T top_k <= 2^30 (2^20 above 1024 experts; ERR_UNSUPPORTED), all
+ * pointers 4-byte aligned, no output overlaps ids or another.  A token may
  * name an expert more than once.  workspace: nvfp4_moe_sort_workspace_size
  * bytes (may be NULL when that is 0), 256-byte aligned, of any content; calls
  * that may overlap need workspaces of their own.  T == 0 or top_k == 0: offsets
@@ -666,10 +671,9 @@ nvfp4_status nvfp4_mx_quantize_rows_bf16(const uint16_t* x, const int32_t* row_t
  * decrease or leave [0, rows]; it is skipped), else -(1 + r) for the first
  * covered row r whose token is outside [0, T).  Where offsets decrease, rows
  * that two experts claim, and those of later experts, may be written or left.
- * The scale byte 0xFF is NaN and makes
- * what reads it NaN.  K % 256 == 0 and K <= 2^22 as for nvfp4_mx_gemm; T K < 2^32,
- * rows and N <= 2^30, E <= 65535 and (rows / 16 + min(E, rows)) ceil(N / 64) <
- * 2^24 (ERR_UNSUPPORTED).
+ * The scale byte 0xFF is NaN and makes what reads it NaN.  K % 256 == 0 and K
+ * <= 2^22 as for nvfp4_mx_gemm; T K < 2^32, rows and N <= 2^30, E <= 65535 and
+ * (rows / 16 + min(E, rows)) ceil(N / 64) < 2^24 (ERR_UNSUPPORTED).
  * a, a_sf, b, b_sf 16-byte aligned, d and bias 2-byte, q 2-byte, the others 4-byte.
  * No workspace.  rows, N (I) or E == 0: nothing but status is written.
  */

@@ -118,6 +118,14 @@ __device__ __forceinline__ double exp_of(double x) { return exp(x); }
 __device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
 __device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
 
+// exp(hi + lo) with the rounding of hi log2 e made up for: within 3 x 2^-24
+// where the result is a normal number.
+__device__ __forceinline__ float exp_fine(float hi, float lo) {
+  const float t = hi * 1.44269504f;
+  const float r = __builtin_fmaf(lo, 1.44269504f, __builtin_fmaf(hi, 1.92596303e-8f, __builtin_fmaf(hi, 1.44269504f, -t)));
+  return __builtin_amdgcn_exp2f(t) * (fabsf(hi) < 200.0f ? __builtin_fmaf(r, 0.69314718f, 1.0f) : 1.0f);
+}
+
 // ----------------------------------------------------------------- scores
 
 // What turns a token's logits into scores: softmax's maximum and the inverse
@@ -128,6 +136,12 @@ struct Scorer {
   bool softmax;
   __device__ __forceinline__ F operator()(float x) const {
     return softmax ? exp_of((F)x - top) * inv : inverse((F)1 + exp_of(-(F)x));
+  }
+  // for a weight: far logits as exactly as near ones
+  __device__ __forceinline__ float fine(float x) const {
+    if (!softmax) return inverse(1.0f + exp_fine(-x, 0.0f));
+    const float d = x - top, b = d - x;  // x - top = d + its rounding
+    return exp_fine(d, (x - (d - b)) - (top + b)) * inv;
   }
 };
 
@@ -352,10 +366,17 @@ __global__ __launch_bounds__(64 * kRouteWaves) __attribute__((amdgpu_waves_per_e
       const Scorer<double> exact = scorer<VPL, double>(x, have, softmax);
       route<VPL, double>(p, x, bias, have, cells[wave], false, exact, none, none, mine);
     }
-    float w = lane < p.top_k ? score(logit_at(p, t * p.ldl + mine)) : 0.0f;
+    const float chosen = lane < p.top_k ? logit_at(p, t * p.ldl + mine) : 0.0f;
+    float w = lane < p.top_k ? score.fine(chosen) : 0.0f;
     if (p.renormalize) {
       const float sum = wave_sum(w);
-      w = sum == 0.0f ? 0.0f : w * inverse(sum);
+      if (sum < 0x1p-90f) {  // uniform; scores below 2^-126 may count
+        const Scorer<double> exact = scorer<VPL, double>(x, have, softmax);
+        const double v = lane < p.top_k ? exact(chosen) : 0.0, all = wave_sum(v);
+        w = all == 0.0 ? 0.0f : (float)(v / all);
+      } else {
+        w = w * inverse(sum);
+      }
     }
     if (lane < p.top_k) {
       p.ids[t * p.top_k + lane] = mine;

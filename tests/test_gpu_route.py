@@ -149,3 +149,46 @@ def test_refused_tensors():
                 dict(bias=torch.zeros(8, device="cuda").bfloat16()), dict(top_k=9), dict(logits=None)):
         with pytest.raises(nv.Nvfp4Error):
             call(**bad)
+
+
+@pytest.mark.parametrize("score", [nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID])
+def test_weights_of_far_logits(score):
+    # every expert is chosen, with weights down to where fp32 ends (below 2^-126 they may be 0)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    for E in (5, 32, 64):
+        logits = torch.randn(20, E, device="cuda", generator=g) * 30
+        for renorm in (True, False):
+            got, w = run(logits, None, score, 1, 1, 1, E, renorm)
+            want, ww = x.route(logits.cpu().numpy(), None, score, 1, 1, 1, E, renorm, 1.0)
+            if score == nv.SCORE_SOFTMAX:  # a sigmoid of more than 37 is 1 in 64 bits, a tie
+                np.testing.assert_array_equal(got, want)
+            else:
+                np.testing.assert_array_equal(np.sort(got, 1), np.sort(want, 1))
+                w, ww = (np.take_along_axis(a, np.argsort(i, 1), 1) for a, i in ((w, got), (ww, want)))
+            # 8 U a score (an exponential within 3, a sum or 1 + it, a reciprocal, a product), the sum's 11
+            # additions of at most 64 of them, its own reciprocal and product
+            assert (np.abs(w - ww) <= 34 * 2.0 ** -24 * ww + 2.0 ** -125).all(), np.max(np.abs(w / ww - 1))
+
+
+def test_renormalised_weights_of_scores_below_fp32():
+    # the bias chooses experts whose scores are 1e-30 .. 1e-300
+    for score in (nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID):
+        for far in (70.0, 87.0, 95.0, 103.0, 300.0, 690.0):
+            logits = torch.zeros(3, 40, device="cuda")
+            logits[:, 10:20] = -far - torch.arange(10, device="cuda") / 8
+            logits[1, 10:20] -= 3
+            logits[2, :10] = 40.0
+            bias = torch.zeros(40, device="cuda")
+            bias[10:20] = 2 + torch.arange(10, device="cuda") / 4
+            got, w = run(logits, bias, score, 1, 1, 1, 6)
+            l, b = logits.cpu().numpy(), bias.cpu().numpy()
+            want, ww = x.route(l, b, score, 1, 1, 1, 6, True, 1.0)
+            np.testing.assert_array_equal(got, want)
+            # Softmax at 690 + 40: scores of 2^-1058, whose 64-bit steps of 2^-1074 are 2^-16 of them.  An
+            # exponential and a product round to such steps, here and in the oracle, by half a step each; a
+            # weight has them in its score and, averaged, in the sum: 8 halves, 4 steps of the smallest score.
+            least = np.take_along_axis(x.scores(l, score), want.astype(np.int64), 1).min(1, keepdims=True)
+            steps = 4 * 2.0 ** -1074 / least
+            assert (np.abs(w - ww) <= (WEIGHT + steps) * ww).all(), (score, far, np.abs(w / ww - 1).max(1), steps)
+    # below what 64 bits hold they are 0
+    assert (run(logits - 1e30, torch.zeros(40, device="cuda"), nv.SCORE_SIGMOID, 1, 1, 1, 6)[1] == 0).all()
