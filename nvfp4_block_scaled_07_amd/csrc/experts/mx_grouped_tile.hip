@@ -1,11 +1,13 @@
 // Grouped products of MXFP4 operands where experts have many rows: 256 rows x
 // 256 weight rows a work-group, 8 waves of 128 x 64, both operands staged in
-// LDS.  Bound by the matrix pipes (65536 rows on 32 experts of 2 x 2048 x 6144:
-// 1012 to 1046 us over boxes, 3.2 PFLOP/s; the plain MX GEMM of 8192^3 3.3 to
-// 3.5), and with a short K by the stores of the outputs as well, which all
-// work-groups issue at the same time (32768 rows of 6144 x 2048 on 64 experts: 407
-// us, 325 without them).  See mx_grouped.hip for the formulas and for the kernel
-// that serves few rows.
+// LDS.  65536 rows on 32 experts of 2 x 2048 x 6144: 1012 to 1046 us over boxes,
+// 3.2 PFLOP/s (the plain MX GEMM of 8192^3: 3.3 to 3.5).  Bound, like that GEMM,
+// by a stage's loads into LDS, its LDS reads and its MFMAs, which overlap only in
+// part (MFMA 35% busy), and with a short K by the stores of the outputs as well,
+// which all work-groups issue at the same time (32768 rows of 6144 x 2048 on 64
+// experts: 407 us, 325 without them).  A stage's scales in 6 reads of 8 bytes
+// instead of 24 of a byte: the same gated, 2% slower plain.  See mx_grouped.hip for
+// the formulas and for the kernel that serves few rows.
 //
 // A's rows are gathered on the way into LDS: the lanes of a load instruction
 // that belong to one row add that row's own offset.  The weights are the MFMA's
