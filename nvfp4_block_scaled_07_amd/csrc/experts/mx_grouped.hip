@@ -15,8 +15,8 @@
 // the codes and the E8M0 bytes as they are.
 //
 // Measured: 64 tokens on 8 of 256 experts of 2 x 2048 x 6144, 2.97 GB of weights
-// in 488 us (6.1 TB/s; a sum over 2 GB reads 6.1), down projections of 6144 x 2048
-// 238 us (6.2); one token 21 and 14 us.
+// in 452 us (6.6 TB/s; a sum over 2 GB reads 6.1), down projections of 6144 x 2048
+// 219 us (6.8); one token 21 and 14 us.
 //
 // The weights are the MFMA's first operand, so a lane ends with four
 // consecutive columns of one row, and an MXFP4 block lies in the registers of
@@ -89,6 +89,7 @@ struct Staged {
 };
 
 constexpr uint32_t kOutside = 0x80000000u;
+constexpr int kStreaming = 2;  // buffer loads that leave the caches to others (non-temporal)
 
 // LDS accesses of this wave done, then a work-group barrier; loads in flight
 // are left alone.
@@ -129,7 +130,8 @@ __device__ __forceinline__ void store_plain(const MxGroupedLaunch& p, int e, int
     if (col >= valid) continue;
     const u4_t w = *(const u4_t*)(out + row * C::kOut + 2 * col);
     uint16_t* to = p.d + (mc + row) * p.N + n0 + col;
-    if (col + 8 <= valid) store8(to, w);
+    // non-temporal: 4096 rows of 6144 columns on 256 experts 324 -> 307 us
+    if (col + 8 <= valid) __builtin_nontemporal_store(w, (u4_any_t*)to);
     else
       for (int j = 0; j < valid - col; ++j) to[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
   }
@@ -309,12 +311,15 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
   };
   const auto unit_load = [&](int u, int unit) {
     const bool live = unit < nu;  // uniform: an empty buffer and no offset else
+    // kStreaming: the weights of an expert of one row tile are used once.  16 tokens on
+    // 256 experts 341 -> 310 us (both products), 37 rows an expert on 64 experts 274 ->
+    // 257; 64 rows, where every other expert has two tiles, 356 -> 368.
 #pragma unroll
     for (int tn = 0; tn < C::TN; ++tn) {
       const rsrc_t r = make_rsrc(C::kGated && tn ? b0 + second * ld : b0, live ? (uint32_t)(valid * ld) : 0u);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        bq[u][tn][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(r, vb[tn][h], live ? unit * 128 : 0, 0));
+        bq[u][tn][h] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(r, vb[tn][h], live ? unit * 128 : 0, kStreaming));
     }
   };
   const auto unit_compute = [&](int buf, int u) {
@@ -393,12 +398,13 @@ template <bool GATED>
 static void launch_rows(const MxGroupedLaunch& p, hipStream_t stream) {
   // The host knows the average rows of an expert only.  Measured (us, both
   // products of a feed-forward of 2048 x 6144, rows on average, by tile height
-  // 16 / 32 / 64 / 256): 2 rows 727 / 734 / 792, 16 rows 1113 / 926 / 973, 64 rows
-  // 729 / 448 / 356 / 377, 80 rows 436 / 383 by the last two, 128 rows 543 / 417
-  // (256 experts up to 16 rows, 64 from there).
+  // 16 / 32 / 64 / 256, with weight loads that stay in the caches): 2 rows 727 / 734 /
+  // 792, 16 rows 1113 / 926 / 973, 64 rows 729 / 448 / 356 / 377, 80 rows 436 / 383 by
+  // the last two, 128 rows 543 / 417 (256 experts up to 16 rows, 64 from there).  As
+  // they are now: 16 rows by 32 867, 37 rows by 64 257, 64 rows 368 by 64 and by 256.
   if (p.rows <= 4 * (int64_t)p.E) launch_stream<16, GATED>(p, stream);
   else if (p.rows <= 24 * (int64_t)p.E) launch_stream<32, GATED>(p, stream);
-  else if (p.rows <= 72 * (int64_t)p.E) launch_stream<64, GATED>(p, stream);
+  else if (p.rows <= 64 * (int64_t)p.E) launch_stream<64, GATED>(p, stream);
   else launch_mx_grouped_tile(p, GATED, stream);
 }
 

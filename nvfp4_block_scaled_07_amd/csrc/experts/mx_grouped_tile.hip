@@ -5,7 +5,7 @@
 // by a stage's loads into LDS, its LDS reads and its MFMAs, which overlap only in
 // part (MFMA 35% busy), and with a short K by the stores of the outputs as well,
 // which all work-groups issue at the same time (32768 rows of 6144 x 2048 on 64
-// experts: 407 us, 325 without them).  A stage's scales in 6 reads of 8 bytes
+// experts: 386 us, 325 without them).  A stage's scales in 6 reads of 8 bytes
 // instead of 24 of a byte: the same gated, 2% slower plain.  See mx_grouped.hip for
 // the formulas and for the kernel that serves few rows.
 //
@@ -272,7 +272,7 @@ __device__ __forceinline__ void finish_tile(const MxGroupedLaunch& p, const Tile
   } else {
     // through LDS, 16 rows of this wave's 64 columns at a time, so that whole
     // 128-byte runs of a row are stored (65536 rows of 6144 x 2048 on 32 experts
-    // 691 us against 782 with 32-byte runs from the accumulators)
+    // 691 us against 782 with 32-byte runs from the accumulators; 641 non-temporal)
     const float alpha = p.alpha ? p.alpha[e] : 1.0f;
     const int col0 = wn * C::kWN;
     const uint16_t* bias = p.bias ? p.bias + (int64_t)e * p.N + n0 + col0 : nullptr;
@@ -309,7 +309,9 @@ __device__ __forceinline__ void finish_tile(const MxGroupedLaunch& p, const Tile
           const int row = wm * C::kWM + tm * 32 + 16 * half + r, col = col0 + k;
           if (row < rows_c && col < t.cols_c) {
             uint16_t* to = p.d + (mc + row) * p.N + n0 + col;
-            if (col + 8 <= t.cols_c) store8(to, x);
+            // non-temporal: the operands keep the caches (32768 rows of 6144 x 2048 on
+            // 64 experts 407 -> 386 us, of 2048 x 768 84 -> 79)
+            if (col + 8 <= t.cols_c) __builtin_nontemporal_store(x, (u4_any_t*)to);
             else
               for (int j = 0; j < t.cols_c - col; ++j) to[j] = (uint16_t)(x[j >> 1] >> (16 * (j & 1)));
           }
