@@ -370,17 +370,23 @@ __global__ __launch_bounds__(64 * kRouteWaves) __attribute__((amdgpu_waves_per_e
     float w = lane < p.top_k ? score.fine(chosen) : 0.0f;
     if (p.renormalize) {
       const float sum = wave_sum(w);
-      if (sum < 0x1p-90f) {  // uniform; scores below 2^-126 may count
+      // A score below 2^-126 counts, in the sum or on its own (over a small sum, or
+      // times a large scale): uniform, and rare, as the logit is then 87 below the
+      // largest (sigmoid: below 0).
+      const bool far = lane < p.top_k && w < 0x1p-126f && chosen != -__builtin_inff();
+      if (sum < 0x1p-90f || __ballot(far) != 0) {
         const Scorer<double> exact = scorer<VPL, double>(x, have, softmax);
         const double v = lane < p.top_k ? exact(chosen) : 0.0, all = wave_sum(v);
-        w = all == 0.0 ? 0.0f : (float)(v / all);
+        w = all == 0.0 ? 0.0f : (float)(v / all * p.scale);
       } else {
-        w = w * inverse(sum);
+        w = w * inverse(sum) * p.scale;
       }
+    } else {
+      w *= p.scale;
     }
     if (lane < p.top_k) {
       p.ids[t * p.top_k + lane] = mine;
-      p.weights[t * p.top_k + lane] = w * p.scale;
+      p.weights[t * p.top_k + lane] = w;
     }
   }
 }

@@ -1,0 +1,44 @@
+"""nvfp4_moe_route where fp32 ends: renormalised weights of chosen scores far
+apart."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_07_amd as nv
+from oracle import experts_ref as x
+from tests.gpu_util import dev, host, say
+from tests.test_gpu_route import WEIGHT, run
+
+pytestmark = pytest.mark.gpu
+
+
+def weights_near(logits, bias, score, k, scale):
+    got, w = run(dev(logits), None if bias is None else dev(bias), score, 1, 1, 1, k, True, scale)
+    want, ww = x.route(logits, bias, score, 1, 1, 1, k, True, scale)
+    np.testing.assert_array_equal(got, want)
+    # the error of a weight, and half a step of fp32 below 2^-126
+    assert (np.abs(w - ww) <= WEIGHT * ww + 2.0 ** -150).all(), (score, k, scale, w, ww)
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 40])
+@pytest.mark.parametrize("score", [nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID])
+def test_renormalised_weights_of_scores_far_apart(score, scale):
+    # the bias chooses experts of these logits: some of their scores are below 2^-126, their sum is not
+    for chosen in ([-61.0, -95.0], [-40.0, -88.0, -89.0], [-62.0, -63.0, -130.0], [-87.0, -87.5], [-3.0, -100.0, -101.0],
+                   [20.0, -95.0, -61.0]):
+        say("far apart", score, scale, chosen)
+        k = len(chosen)
+        logits = np.zeros((2, 40), np.float32)
+        logits[:, 10:10 + k] = chosen
+        logits[1, 39] = 5.0
+        bias = np.zeros(40, np.float32)
+        bias[10:10 + k] = 8.0 - np.arange(k)
+        weights_near(logits, bias, score, k, scale)
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 40])
+def test_renormalised_weights_without_bias(scale):
+    # all experts are chosen, the sum is about 1, and weights times the scale are ordinary numbers
+    logits = -np.array([[0, 1, 30, 80, 87, 88, 95, 100], [0, 90, 91, 92, 93, 94, 95, 96]], np.float32)
+    for score in (nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID):
+        weights_near(logits, None, score, 8, scale)
