@@ -345,6 +345,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) __attribute__((amdgpu_waves_per_e
   int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
   float next[VPL];
   if (t < p.T) load_logits<VPL>(p, t, lane, have, next);
+  float lift = 0.0f;  // largest positive bias
+  if (grouped && p.group_top == 2) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) lift = fmaxf(lift, bias[i]);
+    lift = Key<float>::value(wave_max(Key<float>::of(lift)));
+  }
   for (; t < p.T; t += step) {
     float x[VPL];
 #pragma unroll
@@ -358,7 +364,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) __attribute__((amdgpu_waves_per_e
     // product), and s <= inv.  The sum with the bias is rounded once.
     const float es = softmax ? 0x1p-17f * score.inv : 0x1p-20f;
     const auto slack = [=](float a, float b) { return es + 0x1p-22f * (fabsf(a) + fabsf(b)); };
-    const auto gslack = [=](float a, float b) { return 2.0f * es + 0x1p-21f * (fabsf(a) + fabsf(b)); };
+    // a group's sum also has the rounding of its two values, which a bias can make
+    // far larger than their sum: |a| + |b| <= |a + b| + 2 max(a, 0), a <= score + lift
+    const auto gslack = [=](float a, float b) { return 2.0f * es + 0x1p-21f * (fabsf(a) + fabsf(b) + lift); };
     const auto none = [](auto, auto) { return -__builtin_inff(); };
     int mine = 0;
     const bool clear = route<VPL, float>(p, x, bias, have, (uint32_t*)cells[wave], by_logit, score, slack, gslack, mine);

@@ -1,5 +1,5 @@
 """nvfp4_moe_route where fp32 ends: renormalised weights of chosen scores far
-apart."""
+apart, and group sums of values that cancel."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +7,7 @@ import torch
 import nvfp4_block_scaled_07_amd as nv
 from oracle import experts_ref as x
 from tests.gpu_util import dev, host, say
-from tests.test_gpu_route import WEIGHT, run
+from tests.test_gpu_route import WEIGHT, check, run
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,17 @@ def test_renormalised_weights_without_bias(scale):
     logits = -np.array([[0, 1, 30, 80, 87, 88, 95, 100], [0, 90, 91, 92, 93, 94, 95, 96]], np.float32)
     for score in (nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID):
         weights_near(logits, None, score, 8, scale)
+
+
+def test_group_sums_that_cancel():
+    # groups of two whose biases are opposite: the sums are those of the scores, the values are
+    # thousands, and fp32 has steps of 2^-14 there
+    rng = np.random.default_rng(7)
+    for score in (nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID):
+        for high, groups, kept in ((1000.0, 32, 16), (50.0, 64, 9), (3.0e6, 8, 3)):
+            say("cancelling", score, high, groups, kept)
+            logits = (rng.standard_normal((40, 2 * groups)) * 0.5 / np.sqrt(high)).astype(np.float32)
+            bias = np.zeros(2 * groups, np.float32)
+            bias[0::2] = high + np.arange(groups) * max(1.0, high / 1000)
+            bias[1::2] = -bias[0::2]
+            check(dev(logits), dev(bias), score, groups, kept, 2, min(kept, 8))
