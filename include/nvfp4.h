@@ -606,8 +606,8 @@ nvfp4_status nvfp4_moe_route(const void* logits, int32_t logits_type, int64_t ld
  * nvfp4_moe_sort: the row order that the grouped products and both FFNs take,
  * from ids int32 [T][top_k] (as nvfp4_moe_route writes them, or any others):
  * a stable sort by expert.  Output expert e is id first + e, 0 <= e < E (first
- * = 0: all experts; a GPU that holds a range of them passes its first), ids
- * outside that range are left out:
+ * = 0: all experts; a GPU that holds a range of them passes its first; first + E
+ * <= 2^31), ids outside that range are left out:
  *   offsets int32 [E + 1]: offsets[e] = number of ids of experts below e
  *   row_token int32 [T top_k]: the token of each row (rows at or beyond
  *       offsets[E] are not written)

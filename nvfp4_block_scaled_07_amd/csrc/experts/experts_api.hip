@@ -155,6 +155,8 @@ nvfp4_status nvfp4_moe_sort(const int32_t* ids, int32_t first, int32_t* offsets,
   const char* fn = "nvfp4_moe_sort";
   if (T < 0 || E < 1 || top_k < 0 || first < 0)
     return fail(NVFP4_ERR_SHAPE, "%s: T = %lld, top_k = %d, first = %d must be >= 0 and E = %d >= 1", fn, (ll)T, top_k, first, E);
+  // the kernels compare id - first with E in wrapping 32 bits: no negative id may land below E
+  if (first - 1 > INT32_MAX - E) return fail(NVFP4_ERR_SHAPE, "%s: first = %d, E = %d: first + E is above 2^31", fn, first, E);
   if (E > 65535 || (top_k > 0 && T > kMaxRows / top_k))
     return fail(NVFP4_ERR_UNSUPPORTED, "%s: E = %d, T = %lld, top_k = %d: E up to 65535 and T top_k up to 2^30", fn, E, (ll)T, top_k);
   // a work-group an expert goes through all ids
