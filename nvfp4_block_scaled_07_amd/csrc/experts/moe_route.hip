@@ -173,12 +173,12 @@ __device__ __forceinline__ bool choose(const RouteLaunch& p, typename Key<F>::ty
                                        int& mine) {
   typedef typename Key<F>::type K;
   const int lane = threadIdx.x & 63;
-  K taken = 0;  // lane j: the key of choice j; lane top_k: the best one left
+  K taken = 0, top;  // lane j: the key of choice j; lane top_k: the best one left, which is also the last top
   for (int j = 0;; ++j) {
     K best = key[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) best = kmax(best, key[i]);
-    const K top = wave_max(best);
+    top = wave_max(best);
     taken = lane == j ? top : taken;
     if (j == p.top_k) break;
     const int from = __builtin_ctzll(__ballot(best == top));
@@ -190,7 +190,8 @@ __device__ __forceinline__ bool choose(const RouteLaunch& p, typename Key<F>::ty
     mine = lane == j ? from * VPL + at : mine;
   }
   // the pairs (choice j, choice j + 1), and the last choice with the best one left
-  const K after = __shfl_down(taken, 1);
+  // (64 choices leave no lane for it)
+  const K next = __shfl_down(taken, 1), after = lane == 63 ? top : next;
   const F a = Key<F>::value(taken), b = Key<F>::value(after);
   const bool there = after != 0 && lane < p.top_k;
   return __ballot(there && !(a - b > slack(a, b))) == 0;

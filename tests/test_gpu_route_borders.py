@@ -1,5 +1,6 @@
 """nvfp4_moe_route where fp32 ends: renormalised weights of chosen scores far
-apart, and group sums of values that cancel."""
+apart, group sums of values that cancel, and the last choice of as many as
+there may be."""
 import numpy as np
 import pytest
 import torch
@@ -56,3 +57,31 @@ def test_group_sums_that_cancel():
             bias[0::2] = high + np.arange(groups) * max(1.0, high / 1000)
             bias[1::2] = -bias[0::2]
             check(dev(logits), dev(bias), score, groups, kept, 2, min(kept, 8))
+
+
+def border(rng, score, E, k):
+    """Logits and biases whose values are 0.01 apart but for the k-th and the one after it, which differ
+    by less than fp32 sees: the one of the higher index is the larger."""
+    for _ in range(1000):
+        logits = rng.standard_normal((1, E)).astype(np.float32)
+        order = rng.permutation(E)
+        target = np.empty(E)
+        target[order] = 0.5 + 0.01 * np.arange(E, 0, -1)
+        p, q = sorted(order[k - 1:k + 1])
+        target[q] = target[p] = target[order[k - 1]]
+        s = x.scores(logits, score)[0]
+        bias = (target - s).astype(np.float32)
+        v = s + bias
+        if 0 < v[q] - v[p] < 2e-8:
+            return logits, bias
+    raise AssertionError("no such pair")
+
+
+@pytest.mark.parametrize("score", [nv.SCORE_SOFTMAX, nv.SCORE_SIGMOID])
+@pytest.mark.parametrize("E,k", [(65, 64), (100, 64), (1000, 64), (100, 63), (64, 63), (40, 1), (60, 8)])
+def test_last_choice_that_fp32_cannot_tell(E, k, score):
+    say("border", E, k, score)
+    rng = np.random.default_rng(E + k)
+    for _ in range(5):
+        logits, bias = border(rng, score, E, k)
+        check(dev(np.repeat(logits, 3, 0)), dev(bias), score, 1, 1, 1, k)
