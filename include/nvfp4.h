@@ -651,7 +651,8 @@ nvfp4_status nvfp4_mx_quantize_rows_bf16(const uint16_t* x, const int32_t* row_t
  * 1], of the result belongs to expert e; its A row is row row_token[r] of a
  * (row r if row_token is NULL, then rows <= T), so that a token's activations
  * are quantised and stored once however many experts it has.  Tokens outside
- * [0, T) read as zero rows.
+ * [0, T) read as zero rows (all of them with T == 0; a and a_sf are not read
+ * then, and not NULL all the same).
  *
  * nvfp4_mx_grouped_gemm:
  *   D[r][n] = bf16_rne( alpha[e] * sum_k xA[row(r)][k] * xB_e[n][k] + bias[e][n] )

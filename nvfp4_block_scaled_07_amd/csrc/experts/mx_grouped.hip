@@ -235,8 +235,11 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
 
   rsrc_t ra, ras;
   if (p.row_token) {
-    ra = make_rsrc(p.a, (uint32_t)(p.T * ld));
-    ras = make_rsrc(p.a_sf, (uint32_t)(p.T * lds));
+    // never empty, so that no chunk's scalar offset lies past the end (without
+    // tokens every row's vector offset does)
+    const int64_t most = max(p.T, (int64_t)1);
+    ra = make_rsrc(p.a, (uint32_t)(most * ld));
+    ras = make_rsrc(p.a_sf, (uint32_t)(most * lds));
   } else {
     ra = make_rsrc(p.a + mc * ld, (uint32_t)(rows_c * ld));
     ras = make_rsrc(p.a_sf + mc * lds, (uint32_t)(rows_c * lds));

@@ -185,8 +185,11 @@ __device__ __forceinline__ TileJob<C> tile_job(const MxGroupedLaunch& p, int L, 
   const int64_t row0 = (int64_t)t.e * p.N + t.n0, second = C::kGated ? p.N / 2 : 0;
   t.B = Operand{p.b + row0 * ld, p.b_sf + row0 * lds, ld, lds, t.cols_c, p.b + (row0 + second) * ld, p.b_sf + (row0 + second) * lds};
   const bool gather = p.row_token != nullptr;
-  t.ra = gather ? uniform_rsrc(p.a, (uint32_t)(p.T * ld)) : uniform_rsrc(p.a + t.mc * ld, (uint32_t)(t.rows_c * ld));
-  t.ras = gather ? uniform_rsrc(p.a_sf, (uint32_t)(p.T * lds)) : uniform_rsrc(p.a_sf + t.mc * lds, (uint32_t)(t.rows_c * lds));
+  // never empty, so that no stage's scalar offset lies past the end (without
+  // tokens every row's vector offset does)
+  const int64_t most = gather ? max(p.T, (int64_t)1) : t.rows_c, skip = gather ? 0 : t.mc;
+  t.ra = uniform_rsrc(p.a + skip * ld, (uint32_t)(most * ld));
+  t.ras = uniform_rsrc(p.a_sf + skip * lds, (uint32_t)(most * lds));
   const auto source = [&](int r) -> int64_t {  // row r's row of a, or -1
     if (r >= t.rows_c) return -1;
     if (!gather) return r;
