@@ -584,8 +584,9 @@ nvfp4_status nvfp4_residual_norm(const uint16_t* x, int64_t ldx, const uint16_t*
  * Ties go to the lowest index.  The choice is that of the formulas in 64 bits
  * (values that fp32 cannot tell apart are compared in fp64; where scores alone
  * decide, one by one, their logits are compared, whose order is the scores').
- * Weights are fp32, within a few units of the last place; scores below 2^-126
- * may become 0, but for a renormalised weight they count.
+ * Weights are fp32, within 2^-18 of the formulas' (2^-19 if renormalised or
+ * sigmoid; a few 2^-24 as a rule); scores below 2^-126 may become 0, but for a
+ * renormalised weight they count.
  * A value that is NaN ranks below all others, and top_k different experts
  * always come out.  A NaN or +infinity logit makes softmax weights of its token
  * NaN, and which experts it gets is then not specified; a token whose logits

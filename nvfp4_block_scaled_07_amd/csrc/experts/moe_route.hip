@@ -112,7 +112,8 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 // exp(x): in fp32 the hardware exp2 of the rounded x log2 e, relative error
-// below (|x| + 3) 2^-24
+// below (1.23 |x| + 2) 2^-24 (the product's rounding and the constant's, which is
+// 0.23 of one; one unit of the exponential)
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
 __device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
@@ -330,8 +331,16 @@ __device__ __forceinline__ void load_logits(const RouteLaunch& p, int64_t t, int
 
 constexpr int kRouteWaves = 4;
 
+// Waves a SIMD: a token is a long chain, so more of them hide each other's, up to
+// where registers spill in earnest (four at 256 experts like this, nine with one
+// wave more).  16384 tokens on 256 experts by the compiler's choice (4 waves) 28.0
+// us, 5 waves 25.2, 6 24.9, 7 25.7; 128 experts, 6 / 7 / 8: 15.4 / 16.1 / 16.2; 512
+// experts, 3 / 4 / 5: 38 / 36 / 32; 1024, 2 / 3: 79 / 64.
+constexpr int route_occupancy(int vpl) { return vpl <= 2 ? 7 : vpl == 4 ? 6 : vpl == 8 ? 4 : 2; }
+
 template <int VPL>
-__global__ __launch_bounds__(64 * kRouteWaves) __attribute__((amdgpu_waves_per_eu(VPL <= 2 ? 7 : VPL == 4 ? 6 : VPL == 8 ? 4 : 2))) void k_moe_route(RouteLaunch p) {
+__global__ __launch_bounds__(64 * kRouteWaves) __attribute__((amdgpu_waves_per_eu(route_occupancy(VPL)))) void k_moe_route(
+    RouteLaunch p) {
   __shared__ uint64_t cells[kRouteWaves][64 * VPL];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int have = min(max(p.E - lane * VPL, 0), VPL);  // this lane's experts
@@ -358,11 +367,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) __attribute__((amdgpu_waves_per_e
     for (int i = 0; i < VPL; ++i) x[i] = next[i];
     if (t + step < p.T) load_logits<VPL>(p, t + step, lane, have, next);
     const Scorer<float> score = scorer<VPL, float>(x, have, softmax);
-    // Twice the error of a value.  Sigmoid: with t = exp(-x), s = 1 / (1 + t) is
-    // off by s (t / (1 + t) (|x| + 3) + 3) 2^-24 (hardware exp2 and reciprocal, one
-    // addition), at most 2^-21.5 as s |x| < 0.3 where t is large.  Softmax: below
-    // 2^-18.4 s (two exponentials, a sum of at most 22 additions, a reciprocal, a
-    // product), and s <= inv.  The sum with the bias is rounded once.
+    // Twice the error of a value, in units u = 2^-24.  Sigmoid: the exponential's
+    // error reaches s by s (1 - s), an addition and the reciprocal (two) add 3 s: at
+    // most 3.2 u.  Softmax, of inv: its own exponential, whose argument x - top is
+    // rounded as well, e^-d (2.23 d + 2) <= 2.1, a product 1, and in inv the sum's
+    // exponentials 12 (1023 others at d = 5), its additions 21, the reciprocal 2: 38 u,
+    // and s <= inv.  2^-20 is 16 u, 2^-17 128.  The sum with the bias is rounded once.
     const float es = softmax ? 0x1p-17f * score.inv : 0x1p-20f;
     const auto slack = [=](float a, float b) { return es + 0x1p-22f * (fabsf(a) + fabsf(b)); };
     // a group's sum also has the rounding of its two values, which a bias can make
