@@ -611,7 +611,8 @@ nvfp4_status nvfp4_moe_route(const void* logits, int32_t logits_type, int64_t ld
  * <= 2^31), ids outside that range are left out:
  *   offsets int32 [E + 1]: offsets[e] = number of ids of experts below e
  *   row_token int32 [T top_k]: the token of each row (rows at or beyond
- *       offsets[E] are not written)
+ *       offsets[E] are not written; nvfp4_moe_ffn, whose status looks at every
+ *       row's token, reports them unless the caller put tokens there)
  *   token_rows int32 [T][top_k]: the row of each of a token's experts, -1 for
  *       an id left out (nvfp4_moe_combine and the FFNs add nothing for it)
  * 1 <= E <= 65535, T top_k <= 2^30 (2^20 above 1024 experts; ERR_UNSUPPORTED), all
