@@ -631,7 +631,7 @@ size_t nvfp4_moe_sort_workspace_size(int64_t T, int32_t E, int32_t top_k);
  * MXFP4 quantisation (the operands of nvfp4_mx_gemm): per block of 32
  * consecutive elements of a row, with p its largest magnitude,
  *   e = floor(log2 p) - 2            (NVFP4_MX_FLOOR: OCP Microscaling v1.0; magnitudes above 6 2^e saturate)
- *   e = the least with p <= 6 2^e    (NVFP4_MX_CEIL: nothing saturates)
+ *   e = the least with p <= 6 2^e    (NVFP4_MX_CEIL: nothing up to 6 2^125 saturates)
  * limited to -127 .. 125, scale byte e + 127 and codes e2m1_rne_saturating(x
  * 2^-e) (sign kept, so -0 -> 0x8; a block of zeros has scale byte 0).  A block
  * that holds a NaN gets scale byte 0xFF (NaN) and codes 0; infinities saturate.
@@ -678,7 +678,9 @@ nvfp4_status nvfp4_mx_quantize_rows_bf16(const uint16_t* x, const int32_t* row_t
  * <= 2^22 as for nvfp4_mx_gemm; T K < 2^32, rows and N <= 2^30, E <= 65535 and
  * (rows / 16 + min(E, rows)) ceil(N / 64) < 2^24 (ERR_UNSUPPORTED).
  * a, a_sf, b, b_sf 16-byte aligned, d and bias 2-byte, q 2-byte, the others 4-byte.
- * No workspace.  rows, N (I) or E == 0: nothing but status is written.
+ * No workspace.  rows, N (I) or E == 0: nothing but status is written.  rows / E
+ * chooses the kernel: a holder of a range of the experts that knows offsets[E]
+ * on the host passes it as rows.
  */
 nvfp4_status nvfp4_mx_grouped_gemm(const uint8_t* a, const uint8_t* a_sf, const int32_t* row_token, const uint8_t* b,
                                    const uint8_t* b_sf, const int32_t* offsets, const float* alpha,

@@ -2,10 +2,11 @@
 
 Argument marshalling only: every function passes device pointers, sizes and
 the current HIP stream to the C ABI of ``libnvfp4_gfx950.so`` (built in-tree by
-``nvfp4_block_scaled_07_amd.build``); the calls of the block operators and of the
-mixture-of-experts operators on MXFP4 operands are marshalled by a native module (``_binding``, built with it), the others by ctypes.  All arithmetic runs in the library's
-HIP kernels; there is no CPU or PyTorch fallback, and a missing library is an
-error.
+``nvfp4_block_scaled_07_amd.build``); the calls of the block operators and of
+the mixture-of-experts operators on MXFP4 operands are marshalled by a native
+module (``_binding``, built with it), the others by ctypes.  All arithmetic runs
+in the library's HIP kernels; there is no CPU or PyTorch fallback, and a missing
+library is an error.
 
 The C entry points are exposed with their own names (``nvfp4_gemm``,
 ``nvfp4_grouped_gemm``, ...) taking torch tensors in place of pointers.
@@ -546,8 +547,9 @@ _bind = None
 
 def _native():
     """The native marshalling module of the block operators and the
-    mixture-of-experts operators (csrc/binding.cpp), bound to the loaded library; raises if it has not been built, does not
-    load or was built for another torch."""
+    mixture-of-experts operators (csrc/binding.cpp), bound to the loaded
+    library; raises if it has not been built, does not load or was built for
+    another torch."""
     global _bind
     if _bind is None:
         import torch

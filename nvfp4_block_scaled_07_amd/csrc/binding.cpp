@@ -1,5 +1,6 @@
 // Native marshalling of the Python calls of the block operators and of the
-// mixture-of-experts operators on MXFP4 operands: torch tensors to the addresses, sizes and stream that the C ABI of include/nvfp4.h takes.  A
+// mixture-of-experts operators on MXFP4 operands: torch tensors to the
+// addresses, sizes and stream that the C ABI of include/nvfp4.h takes.  A
 // decode step makes hundreds of these calls back to back, each a few
 // microseconds of GPU work; the same checks and argument conversion through
 // ctypes took 4.5 us a call, as long as the launch itself.

@@ -232,8 +232,11 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortLaunch p, int r
 }
 
 // Whether the second form is taken.  256 experts, us by the first and the second
-// form: 8192 ids 5.1 and 12.9, 32768 ids 11.0 and 13.3, 131072 ids 36.8 and 16.9, a
-// million 288 and 40; 16 experts, 131072 ids: 50 and 12.3.
+// form: 8192 ids 5.1 and 12.6, 32768 ids 11.0 and 13.3, 49152 ids 15.1 and 15.8, 65536
+// ids 19.7 and 14.6, 131072 ids 36.8 and 17.1, a million 288 and 40.  At 40960 ids, 16
+// experts 17.4 and 11.7, 64 15.4 and 12.4, 128 14.2 and 14.4, 512 18.5 and 16.3, 1024
+// 31.6 and 18.1: the border is that of 128 to 256 experts, others meet earlier (16 at
+// 24576 ids, 512 at 32768, 1024 at 16384).
 static bool many_ids(int64_t n, int E) { return n > 40960 && E <= kMostSorted; }
 
 size_t moe_sort_workspace(int64_t n, int E) {

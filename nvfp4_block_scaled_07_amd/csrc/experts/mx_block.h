@@ -5,7 +5,7 @@
 // 127), the codes are e2m1_rne(x 2^-e), saturating, sign kept.  e is
 //   rule 0: floor(log2 p) - 2, the OCP Microscaling v1.0 conversion: p 2^-e
 //           lies in [4, 8), what lies above 6 saturates;
-//   rule 1: the least e with p <= 6 2^e, so that nothing saturates;
+//   rule 1: the least e with p <= 6 2^e, so that nothing up to 6 2^125 saturates;
 // limited to bytes 0 .. 252 (252: the largest scale whose codes are all finite
 // fp32 values).  2^-e is a power of two, so x 2^-e is exact (bytes 0 .. 252
 // give 2^127 .. 2^-125; a product that underflows is far below the rounding to

@@ -316,7 +316,8 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(C::
     const bool live = unit < nu;  // uniform: an empty buffer and no offset else
     // kStreaming: the weights of an expert of one row tile are used once.  16 tokens on
     // 256 experts 341 -> 310 us (both products), 37 rows an expert on 64 experts 274 ->
-    // 257; 64 rows, where every other expert has two tiles, 356 -> 368.
+    // 257; 64 rows, where every other expert has two tiles, 356 -> 368: at every tile
+    // height, as the rows of single experts are not known here.
 #pragma unroll
     for (int tn = 0; tn < C::TN; ++tn) {
       const rsrc_t r = make_rsrc(C::kGated && tn ? b0 + second * ld : b0, live ? (uint32_t)(valid * ld) : 0u);
@@ -399,7 +400,11 @@ static void launch_stream(const MxGroupedLaunch& p, hipStream_t stream) {
 
 template <bool GATED>
 static void launch_rows(const MxGroupedLaunch& p, hipStream_t stream) {
-  // The host knows the average rows of an expert only.  Measured (us, both
+  // The host knows rows and E, whose quotient is the average rows of an expert if
+  // all rows are these experts'.  With a range of the experts, rows that others have
+  // count as well, and the tiles may be too high: 32 of 256 experts of 2 x 2048 x 6144,
+  // 8 a token, both products by top_k T rows and by those that exist, 16 tokens 55 and
+  // 55 us, 64 106 and 102, 128 123 and 109, 512 188 and 113.  Measured (us, both
   // products of a feed-forward of 2048 x 6144, rows on average, by tile height
   // 16 / 32 / 64 / 256, with weight loads that stay in the caches): 2 rows 727 / 734 /
   // 792, 16 rows 1113 / 926 / 973, 64 rows 729 / 448 / 356 / 377, 80 rows 436 / 383 by
